@@ -68,9 +68,10 @@ typedef enum {
 } yoco_status_t;
 
 /* YOCO_E4M3 names the 8-bit cache of the *_e4m3 calls (bf16 queries and
- * outputs over an e4m3 cache); only yoco_cross_attn_workspace_size and
- * yoco_cross_decoder_bytes take it. */
-typedef enum { YOCO_F32 = 0, YOCO_BF16 = 1, YOCO_E4M3 = 2 } yoco_dtype_t;
+ * outputs over an e4m3 cache), YOCO_E2M1 the 4-bit cache of the *_e2m1
+ * calls; yoco_cross_attn_workspace_size, yoco_cross_attn_plan and
+ * yoco_cross_decoder_bytes take both, yoco_cross_decode_step YOCO_E4M3. */
+typedef enum { YOCO_F32 = 0, YOCO_BF16 = 1, YOCO_E4M3 = 2, YOCO_E2M1 = 3 } yoco_dtype_t;
 
 /* Flags of yoco_cross_attn_paged. */
 #define YOCO_ATTN_REVERSE 0x1u /* tensor-core paths: walk each worker's pages last to first */
@@ -87,6 +88,7 @@ typedef enum { YOCO_F32 = 0, YOCO_BF16 = 1, YOCO_E4M3 = 2 } yoco_dtype_t;
 #define YOCO_DEVERR_TIMEOUT 0x10     /* a bounded wait on an asynchronous copy gave up */
 #define YOCO_DEVERR_SCALE 0x20       /* e4m3 cache: a page scale outside the supported range */
 #define YOCO_DEVERR_PLAN 0x40        /* YOCO_ATTN_PLANNED, but the workspace holds no plan for these shapes */
+#define YOCO_DEVERR_NO_PAGES 0x80    /* yoco_build_block_tables: the free pages do not cover the step */
 
 /*
  * yoco_kv_append — write the step's new shared K^/V^ into the paged cache.
@@ -140,8 +142,8 @@ yoco_status_t yoco_select_cross_rows(const int32_t* query_start_loc, const int32
  * yoco_cross_attn_workspace_size — bytes of fp32 scratch that
  * yoco_cross_attn_paged needs for these bounds on the current device (the
  * split-KV partial outputs and their log-sum-exp statistics). Returns 0 for
- * unsupported or invalid arguments. dtype YOCO_E4M3 sizes the scratch of
- * yoco_cross_attn_paged_e4m3.
+ * unsupported or invalid arguments. dtype YOCO_E4M3 (YOCO_E2M1) sizes the
+ * scratch of yoco_cross_attn_paged_e4m3 (_e2m1).
  */
 size_t yoco_cross_attn_workspace_size(int32_t max_rows, int32_t num_q_heads, int32_t num_kv_heads,
                                       int32_t head_dim, int32_t block_size, int32_t max_seq_len,
@@ -240,7 +242,7 @@ yoco_status_t yoco_cross_attn_paged(const void* q, const void* k_cache, const vo
  * segment, and the CTAs' arrival counters. The layers then pass
  * YOCO_ATTN_PLANNED and start streaming after one dependent load.
  *   arguments    as for yoco_cross_attn_paged (the same values the layers will pass);
- *                dtype YOCO_BF16 or YOCO_E4M3 (the e4m3 layers' own kernel shape);
+ *                dtype YOCO_BF16, YOCO_E4M3 or YOCO_E2M1 (each cache's own kernel shape);
  *                YOCO_F32 needs no plan and returns YOCO_OK without a launch
  *   flags        0 or YOCO_ATTN_OVERLAP (the previous kernel on `stream` writes none of
  *                block_table, seq_lens, cross_query_start_loc; the plan is written after it
@@ -313,6 +315,130 @@ yoco_status_t yoco_kv_append_e4m3(const void* k_new, const void* v_new, void* k_
  */
 yoco_status_t yoco_cross_attn_paged_e4m3(const void* q, const void* k_cache, const void* v_cache,
                                          const float* page_scales, void* out,
+                                         const int32_t* block_table, int32_t max_blocks_per_req,
+                                         const int32_t* seq_lens,
+                                         const int32_t* cross_query_start_loc, int32_t num_reqs,
+                                         int32_t max_rows, int32_t max_seq_len,
+                                         int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                         float scale, uint32_t flags, void* workspace,
+                                         size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/*
+ * yoco_build_block_tables — extend the block tables by the pages a step's
+ * tokens need and give every token its slot, on the GPU, from lengths alone.
+ *
+ * "KV cache memory systems", "Contiguous allocation wastes capacity": a
+ * request's logical blocks map through its block table to physical pages
+ * handed out as it grows; "You Only Cache Once, in vLLM" names the step's
+ * block_table_tensor and slot_mapping. With q = q_len of request r:
+ *   held = ceil((seq_lens[r] - q) / block_size)   pages its row already holds
+ *   need = ceil(seq_lens[r] / block_size)         pages after this step
+ * The pages held..need-1 of all requests, in request order, are taken one by
+ * one from the top of the free stack: the n-th page of the step (from 0) is
+ * free_pages[num_free - 1 - n]. Token j of request r, at position
+ * p = seq_lens[r] - q + j, gets
+ *   slot_mapping[qsl[r] + j] = page(p / block_size) * block_size + p % block_size.
+ *   block_table     device int32 [num_reqs][max_blocks_per_req], in and out: entries
+ *                   0..held-1 are read, held..need-1 written, the rest left as they were
+ *   seq_lens, query_start_loc  device int32, as for yoco_kv_append
+ *   num_tokens      host, length of slot_mapping; tokens from query_start_loc[num_reqs] on
+ *                   (padding of a captured graph) get slot -1
+ *   free_pages      device int32 [free_capacity], a stack of free physical pages (bottom
+ *                   first), or NULL: no page is taken, the rows must already hold them all
+ *   num_free        device int32 [1]: pages on the stack
+ *   num_free_after  device int32 [1] out: pages left. Another word than num_free: exchange
+ *                   the two from step to step (both are ignored without free_pages)
+ *   slot_mapping    device int32 [num_tokens] out; -1 for a token without a slot
+ *   err_word        device int32 or NULL
+ * A request that schedules no token is not looked at. A request whose pages
+ * are not covered (the running count of the step's pages up to it exceeds
+ * num_free), and every later one that needs a page, gets none: its row stays,
+ * its tokens get -1, YOCO_DEVERR_NO_PAGES is set. Lengths with seq_len <
+ * q_len or beyond the row set YOCO_DEVERR_POS_RANGE, malformed offsets (or a
+ * num_free outside [0, free_capacity]) YOCO_DEVERR_OFFSETS, a page outside
+ * [0, num_blocks) YOCO_DEVERR_PAGE_RANGE; the tokens concerned get -1 (a bad
+ * page from the stack is entered as -1), and such lengths take no page.
+ * num_blocks * block_size is at most 2^31 - 1. One launch; exact and
+ * independent of timing.
+ */
+yoco_status_t yoco_build_block_tables(int32_t* block_table, int32_t max_blocks_per_req,
+                                      const int32_t* seq_lens, const int32_t* query_start_loc,
+                                      int32_t num_reqs, int32_t num_tokens, int32_t num_blocks,
+                                      int32_t block_size, const int32_t* free_pages,
+                                      int32_t free_capacity, const int32_t* num_free,
+                                      int32_t* num_free_after, int32_t* slot_mapping,
+                                      int32_t* err_word, void* stream);
+
+/*
+ * 4-bit cache: e2m1 K^/V^ with a power-of-two scale for 32 head dims
+ * ---------------------------------------------------------------------
+ * "KV cache memory systems", "Quantized cache changes attention inputs": a
+ * quantized cache cuts the bytes per cached scalar and adds scale metadata.
+ * 4.25 bits an element, so a layer streams 0.27 of a bf16 cache's bytes.
+ *   - An element is an e2m1 code (1 sign, 2 exponent bits, 1 mantissa bit:
+ *     0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; no infinity, no NaN).
+ *     32 consecutive head dims of a token's K^ (V^) row of one kv head share
+ *     a scale 2^(b - 127), b a byte: the OCP microscaling block.
+ *   - Pools k_cache, v_cache: uint8 [num_blocks][num_kv_heads][block_size]
+ *     [head_dim / 2], two codes a byte, the even head dim in the low half.
+ *   - block_scales: uint8 [num_blocks][num_kv_heads][2][block_size]
+ *     [head_dim / 32], the bytes b of K^ and then of V^.
+ *   - head_dim 128 or 256; block_size 16 or 32; groups up to 16.
+ * The scales come from the values themselves: nothing is calibrated.
+ */
+
+/*
+ * yoco_kv_append_e2m1 — write a step's new K^/V^ rows into the 4-bit cache.
+ * For each 32 head dims, b is the smallest byte in [1, 251] with every
+ * magnitude at most 6 * 2^(b - 127) (251 where there is none), and each code
+ * the e2m1 value nearest to value * 2^(127 - b), ties to the even code,
+ * saturating at 6; infinities and NaN count as the largest finite value of
+ * their sign.
+ *   k_new, v_new    device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte aligned
+ *   k_cache, v_cache, block_scales  device (above), 16-byte aligned
+ *   slot_mapping    device int32 [num_tokens] (from yoco_build_block_tables): token t goes to
+ *                   slot slot_mapping[t] % block_size of page slot_mapping[t] / block_size;
+ *                   a negative slot is skipped, one past the pool sets
+ *                   YOCO_DEVERR_PAGE_RANGE. Slots are distinct (else which row stays is open).
+ */
+yoco_status_t yoco_kv_append_e2m1(const void* k_new, const void* v_new, void* k_cache,
+                                  void* v_cache, void* block_scales, const int32_t* slot_mapping,
+                                  int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t* err_word,
+                                  void* stream);
+
+/*
+ * yoco_kv_gather_e2m1 — read rows of the 4-bit cache back as values: row t of
+ * k_out, v_out (device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte
+ * aligned) becomes code * scale of slot slot_mapping[t], exactly; a negative
+ * slot, or one past the pool (YOCO_DEVERR_PAGE_RANGE), gives a row of zeros.
+ * A slot may be read any number of times. Other arguments as for
+ * yoco_kv_append_e2m1.
+ */
+yoco_status_t yoco_kv_gather_e2m1(const void* k_cache, const void* v_cache,
+                                  const void* block_scales, const int32_t* slot_mapping,
+                                  void* k_out, void* v_out, int32_t num_tokens, int32_t num_blocks,
+                                  int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                                  int32_t* err_word, void* stream);
+
+/*
+ * yoco_cross_attn_paged_e2m1 — yoco_cross_attn_paged over a 4-bit cache:
+ * out = softmax(scale * q K^T) V with K, V = code * 2^(b - 127).
+ *   q, out        device bf16 [max_rows][num_q_heads][head_dim]
+ *   k_cache, v_cache, block_scales  as for yoco_kv_append_e2m1
+ *   workspace     >= yoco_cross_attn_workspace_size(..., YOCO_E2M1) bytes
+ * Scale bytes of tokens in reach must lie in [1, 251] (the append writes no
+ * others): other bytes give an undefined result, never a fault. Arithmetic:
+ * codes widen exactly to f16; each query head is brought into f16's range by
+ * a power of two and is exact there but for elements 2^29 below its largest;
+ * products and sums in fp32, a block's sum taking its K scale in fp32;
+ * softmax weights round to f16 (under 2^-32 of the largest they are gone), and
+ * V scales more than 2^21 below the largest that a walk has met count for nothing. Everything else (flags,
+ * errors, determinism) is as for yoco_cross_attn_paged.
+ */
+yoco_status_t yoco_cross_attn_paged_e2m1(const void* q, const void* k_cache, const void* v_cache,
+                                         const void* block_scales, void* out,
                                          const int32_t* block_table, int32_t max_blocks_per_req,
                                          const int32_t* seq_lens,
                                          const int32_t* cross_query_start_loc, int32_t num_reqs,
@@ -436,7 +562,8 @@ yoco_status_t yoco_set_l2_window(void* stream, void* base, size_t bytes, float h
  * with elem = 2 (bf16) or 4 (fp32); a request with no row moves nothing. For
  * one row per request this is each row's own causal prefix. For YOCO_E4M3 the
  * K^/V^ term uses 1 byte per element, the query/output term 2, and each page
- * adds its 16-byte scale record next to its block-table entry.
+ * adds its 16-byte scale record next to its block-table entry; for YOCO_E2M1
+ * half a byte per element, 2, and 2 * block_size * head_dim / 32 scale bytes.
  *   query_start_loc, seq_lens   host int32 [num_reqs + 1] / [num_reqs]
  *   rows_per_req                host int32 [num_reqs] or NULL (= 1)
  *   per_req_bytes               host int64 out [num_reqs] or NULL

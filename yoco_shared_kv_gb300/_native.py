@@ -18,7 +18,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libyoco_kv.so")
 
 YOCO_OK, YOCO_ERR_INVALID_ARG, YOCO_ERR_UNSUPPORTED, YOCO_ERR_WORKSPACE, YOCO_ERR_CUDA = range(5)
-YOCO_F32, YOCO_BF16, YOCO_E4M3 = 0, 1, 2
+YOCO_F32, YOCO_BF16, YOCO_E4M3, YOCO_E2M1 = 0, 1, 2, 3
+E2M1 = torch.float4_e2m1fn_x2  # names the 4-bit cache where a call takes a cache's dtype
 YOCO_ATTN_REVERSE = 0x1
 YOCO_ATTN_OVERLAP = 0x2
 YOCO_ATTN_KEEP_TAIL = 0x4
@@ -30,13 +31,16 @@ DEVERR_OFFSETS = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_SCALE = 0x20
 DEVERR_PLAN = 0x40
+DEVERR_NO_PAGES = 0x80
 
 EXPORTED = ("yoco_kv_append", "yoco_select_cross_rows", "yoco_cross_attn_workspace_size",
             "yoco_cross_attn_paged", "yoco_set_l2_window", "yoco_status_string", "yoco_version",
             "yoco_last_cuda_error", "yoco_last_cuda_error_string",
             "yoco_cross_attn_paged_noalloc", "yoco_cross_attn_noalloc_capacity",
             "yoco_selftest_wait_timeout", "yoco_cross_decoder_bytes", "yoco_kv_append_e4m3",
-            "yoco_cross_attn_paged_e4m3", "yoco_cross_decode_step", "yoco_cross_attn_plan")
+            "yoco_cross_attn_paged_e4m3", "yoco_cross_decode_step", "yoco_cross_attn_plan",
+            "yoco_build_block_tables", "yoco_kv_append_e2m1", "yoco_kv_gather_e2m1",
+            "yoco_cross_attn_paged_e2m1")
 
 
 class YocoError(RuntimeError):
@@ -100,6 +104,17 @@ def _load() -> ctypes.CDLL:
     L.yoco_cross_attn_paged_e4m3.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32,
                                              i32, i32, i32, i32, i32, ctypes.c_float,
                                              ctypes.c_uint32, vp, sz, vp, vp]
+    L.yoco_build_block_tables.restype = ctypes.c_int
+    L.yoco_build_block_tables.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp,
+                                          vp, vp]
+    L.yoco_kv_append_e2m1.restype = ctypes.c_int
+    L.yoco_kv_append_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    L.yoco_kv_gather_e2m1.restype = ctypes.c_int
+    L.yoco_kv_gather_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp]
+    L.yoco_cross_attn_paged_e2m1.restype = ctypes.c_int
+    L.yoco_cross_attn_paged_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32,
+                                             i32, i32, i32, i32, i32, ctypes.c_float,
+                                             ctypes.c_uint32, vp, sz, vp, vp]
     return L
 
 
@@ -116,13 +131,16 @@ def _check(fn: str, status: int) -> None:
 
 
 def dtype_code(t: torch.dtype) -> int:
-    """bf16 / fp32 caches; torch.float8_e4m3fn (or uint8) names the e4m3 cache."""
+    """bf16 / fp32 caches; torch.float8_e4m3fn (or uint8) names the e4m3 cache, E2M1
+    (torch.float4_e2m1fn_x2) the 4-bit one."""
     if t == torch.bfloat16:
         return YOCO_BF16
     if t == torch.float32:
         return YOCO_F32
     if t in (torch.float8_e4m3fn, torch.uint8):
         return YOCO_E4M3
+    if t == E2M1:
+        return YOCO_E2M1
     raise ValueError(f"unsupported dtype {t}")
 
 
@@ -366,3 +384,101 @@ def yoco_cross_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
         num_blocks, float(scale), YOCO_E4M3 if e4m3 else YOCO_BF16, int(flags), _ptr(workspace),
         ws_bytes, None if err_word is None else _i32(err_word, "err_word"), _stream(stream)))
 
+
+
+def _arg(t: Optional[torch.Tensor], dtype: torch.dtype, shape, name: str) -> Optional[int]:
+    """Pointer of a contiguous tensor of this dtype and shape on the current device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}: got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return t.data_ptr()
+
+
+def yoco_build_block_tables(block_table: torch.Tensor, seq_lens: torch.Tensor,
+                            query_start_loc: torch.Tensor, num_blocks: int, block_size: int,
+                            slot_mapping: torch.Tensor, free_pages: Optional[torch.Tensor] = None,
+                            num_free: Optional[torch.Tensor] = None,
+                            num_free_after: Optional[torch.Tensor] = None,
+                            err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Extend ``block_table [R, max_blocks]`` by the pages the step's tokens need (from the
+    stack ``free_pages[:num_free]``, or none when it is None) and fill ``slot_mapping [T]``."""
+    i32 = torch.int32
+    R, max_blocks = block_table.shape
+    T = slot_mapping.numel()
+    cap = 0 if free_pages is None else free_pages.numel()
+    _check("yoco_build_block_tables", lib.yoco_build_block_tables(
+        _arg(block_table, i32, (R, max_blocks), "block_table"), max_blocks,
+        _arg(seq_lens, i32, (R,), "seq_lens"), _arg(query_start_loc, i32, (R + 1,), "query_start_loc"),
+        R, T, int(num_blocks), int(block_size), _arg(free_pages, i32, (cap,), "free_pages"), cap,
+        _arg(num_free, i32, (1,), "num_free"), _arg(num_free_after, i32, (1,), "num_free_after"),
+        _arg(slot_mapping, i32, (T,), "slot_mapping"), _arg(err_word, i32, (1,), "err_word"),
+        _stream(stream)))
+
+
+def _e2m1_pools(k_cache: torch.Tensor, v_cache: torch.Tensor, block_scales: torch.Tensor):
+    """(pointers, num_blocks, H_kv, block_size, D) of a 4-bit cache."""
+    u8 = torch.uint8
+    num_blocks, H_kv, bs, half = k_cache.shape
+    shape = (num_blocks, H_kv, bs, half)
+    ptrs = (_arg(k_cache, u8, shape, "k_cache"), _arg(v_cache, u8, shape, "v_cache"),
+            _arg(block_scales, u8, (num_blocks, H_kv, 2, bs, half // 16), "block_scales"))
+    return ptrs, num_blocks, H_kv, bs, 2 * half
+
+
+def yoco_kv_append_e2m1(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, block_scales: torch.Tensor,
+                        slot_mapping: torch.Tensor, err_word: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Quantising append: bf16 ``k_new/v_new [T, H_kv, D]`` into 4-bit pools
+    ``[num_blocks, H_kv, bs, D / 2]`` with scale bytes ``[num_blocks, H_kv, 2, bs, D / 32]``."""
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    T = slot_mapping.numel()
+    _check("yoco_kv_append_e2m1", lib.yoco_kv_append_e2m1(
+        _arg(k_new, torch.bfloat16, (T, H_kv, D), "k_new"),
+        _arg(v_new, torch.bfloat16, (T, H_kv, D), "v_new"), *pools,
+        _arg(slot_mapping, torch.int32, (T,), "slot_mapping"), T, num_blocks, bs, H_kv, D,
+        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+
+
+def yoco_kv_gather_e2m1(k_cache: torch.Tensor, v_cache: torch.Tensor, block_scales: torch.Tensor,
+                        slot_mapping: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+                        err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of a 4-bit cache as the bf16 values they stand for: ``k_out/v_out [T, H_kv, D]``."""
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    T = slot_mapping.numel()
+    _check("yoco_kv_gather_e2m1", lib.yoco_kv_gather_e2m1(
+        *pools, _arg(slot_mapping, torch.int32, (T,), "slot_mapping"),
+        _arg(k_out, torch.bfloat16, (T, H_kv, D), "k_out"),
+        _arg(v_out, torch.bfloat16, (T, H_kv, D), "v_out"), T, num_blocks, bs, H_kv, D,
+        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+
+
+def yoco_cross_attn_paged_e2m1(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               block_scales: torch.Tensor, out: torch.Tensor,
+                               block_table: torch.Tensor, seq_lens: torch.Tensor,
+                               cross_query_start_loc: torch.Tensor, max_seq_len: int, scale: float,
+                               workspace: Optional[torch.Tensor],
+                               err_word: Optional[torch.Tensor] = None, stream=None,
+                               max_rows: Optional[int] = None, flags: int = 0) -> None:
+    """One layer over a 4-bit cache: bf16 ``q/out [max_rows, H_q, D]``."""
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    rows_cap, H_q = q.shape[:2]
+    R, max_blocks = block_table.shape
+    max_rows = rows_cap if max_rows is None else int(max_rows)
+    if max_rows > rows_cap:
+        raise ValueError("max_rows is more than q holds")
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    _check("yoco_cross_attn_paged_e2m1", lib.yoco_cross_attn_paged_e2m1(
+        _arg(q, torch.bfloat16, (rows_cap, H_q, D), "q"), *pools,
+        _arg(out, torch.bfloat16, (rows_cap, H_q, D), "out"),
+        _arg(block_table, torch.int32, (R, max_blocks), "block_table"), max_blocks,
+        _arg(seq_lens, torch.int32, (R,), "seq_lens"),
+        _arg(cross_query_start_loc, torch.int32, (R + 1,), "cross_query_start_loc"), R, max_rows,
+        int(max_seq_len), H_q, H_kv, D, bs, num_blocks, float(scale), int(flags),
+        _arg(workspace, torch.uint8, (ws_bytes,), "workspace"), ws_bytes,
+        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))

@@ -5,6 +5,9 @@
 
 namespace yoco {
 
+// What the cache of the tensor-core path holds.
+constexpr int kBf16 = 0, kE4m3 = 1, kE2m1 = 2;
+
 // Launch parameters common to both attention paths.
 struct AttnParams {
     const void* q;              // [max_rows][H_q][D]
@@ -31,7 +34,8 @@ struct AttnParams {
     int32_t split_pages;        // CUDA-core path: logical pages per split
     int32_t max_splits;         // CUDA-core path
     int32_t max_seq_len;        // host bound on seq_lens (the CUDA-core split plan is sized by it)
-    const float4* scales;       // e4m3 cache: {k_scale, v_scale, -, -} per (page, kv head)
+    const float4* scales;       // e4m3 cache: {k_scale, v_scale, -, -} per (page, kv head);
+                                // e2m1 cache: scale bytes [K, V][block_size][D / 32] of each
     float scale_log2;           // softmax scale * log2(e)
     int32_t reverse;            // tensor-core path: walk each worker's pages from the end
     int32_t overlap;            // tensor-core path: launch as a programmatic dependent
@@ -61,11 +65,13 @@ __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
 
 // Host-side launchers (one per path). `tc_workspace_bytes` / `cc_*` give the
 // scratch each path needs.
-size_t tc_workspace_bytes(int sms, int H_kv, int G, int D, int BS, bool e4m3);
+size_t tc_workspace_bytes(int sms, int H_kv, int G, int D, int BS, int format);
 int tc_ctas(int sms);
 cudaError_t launch_attn_tc(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p,
                            int D, int BS, int sms, cudaStream_t s);
 cudaError_t launch_attn_tc_e4m3(const CUtensorMap& mk, const CUtensorMap& mv,
+                                const AttnParams& p, int D, int BS, int sms, cudaStream_t s);
+cudaError_t launch_attn_tc_e2m1(const CUtensorMap& mk, const CUtensorMap& mv,
                                 const AttnParams& p, int D, int BS, int sms, cudaStream_t s);
 cudaError_t launch_attn_cc(const void* k_cache, const void* v_cache, const AttnParams& p, int D,
                            int hb, cudaStream_t s);

@@ -74,17 +74,39 @@ namespace {
 #ifndef YOCO_TC_F8_RING
 #define YOCO_TC_F8_RING 196608
 #endif
+// e2m1 cache: warps per CTA (head_dim 128 with one and with two 8-head tiles,
+// head_dim 256 with one tile and as warp pairs), and shared-memory bytes of
+// the warps' stages
+#ifndef YOCO_TC_F4_NW128
+#define YOCO_TC_F4_NW128 16
+#endif
+#ifndef YOCO_TC_F4_NW128W
+#define YOCO_TC_F4_NW128W 8
+#endif
+#ifndef YOCO_TC_F4_NW256
+#define YOCO_TC_F4_NW256 12
+#endif
+#ifndef YOCO_TC_F4_NW256P
+#define YOCO_TC_F4_NW256P 8
+#endif
+#ifndef YOCO_TC_F4_RING
+#define YOCO_TC_F4_RING 196608
+#endif
 
-// F8: the cache holds e4m3 bytes (one byte per element) instead of bf16.
+
+// FMT: what the cache holds: bf16, e4m3 (F8: one byte per element) or e2m1
+// (F4: two elements per byte, one scale byte per 32 head dims of a token).
 // NT: 8-head tiles of a warp (1 for groups up to 8, else 2).
 // PR: warp pairs (NT = 1): the two warps of a pair walk the same pages from
 // one ring, each taking one of the group's two 8-head tiles, so a 16-column
 // walk runs on twice the warps in the same shared memory.
-template <int D, int BS, bool F8 = false, int NT = 2, bool PR = false>
+template <int D, int BS, int FMT = kBf16, int NT = 2, bool PR = false>
 struct TcShape {
+    static constexpr bool F8 = FMT == kE4m3, F4 = FMT == kE2m1;
     static_assert(!PR || NT == 1, "a warp of a pair takes one 8-head tile");
-    static constexpr int ESZ = F8 ? 1 : 2;                // bytes per cached element
-    static constexpr int PAGE_BYTES = BS * D * ESZ;       // K (or V) of one page, one kv head
+    static constexpr int ESZ = F8 ? 1 : 2;                // bytes per cached element (not e2m1)
+    static constexpr int ROW_BYTES = F4 ? D / 2 : D * ESZ;  // K (or V) of one token, one kv head
+    static constexpr int PAGE_BYTES = BS * ROW_BYTES;     // K (or V) of one page, one kv head
     static constexpr int STAGE_BYTES = 2 * PAGE_BYTES;    // K + V
     static constexpr int NTG = PR ? 2 : NT;               // 8-head tiles of the group
     // a worker's (warp's, or pair's) two end-of-slice pieces at the largest group
@@ -99,21 +121,32 @@ struct TcShape {
     // Two 8-head tiles of one warp at head_dim 256 hold the queries in shared
     // memory (below): their kernels keep 4 warps x 3 stages whatever the
     // tunables say; so do the pair kernels (4 pairs x 3 stages).
-    static constexpr bool QSM = D == 256 && NT == 2;
+    static constexpr bool QSM = D == 256 && NT == 2 && !F4;
+    // e2m1: as many warps as the registers of their accumulators allow (the walk is
+    // bound by instructions, not by the bytes in flight)
+    static constexpr int F4_NW = D == 256 ? (NTG == 2 ? YOCO_TC_F4_NW256P / 2 : YOCO_TC_F4_NW256)
+                                          : (NTG == 2 ? YOCO_TC_F4_NW128W / (PR ? 2 : 1) : YOCO_TC_F4_NW128);
+    static constexpr int F4_SREC = 2 * BS * (D / 32);  // scale bytes of a (page, kv head): K, then V
     // workers (each with its own ring and slice), and warps
     static constexpr int WK =
-        F8 ? F8_NW
+        F4 ? F4_NW
+        : F8 ? F8_NW
            : (STAGE_BYTES <= 8192 ? 8
                                   : (STAGE_BYTES <= 16384 ? ((QSM || PR) ? 4 : YOCO_TC_NW16) : 2));
     static constexpr int NW = PR ? 2 * WK : WK;
     // e4m3 pages are small: deepen the ring to keep ~192 KiB in flight per SM
     static constexpr int F8_STAGES = YOCO_TC_F8_RING / F8_NW / STAGE_BYTES;
+    static constexpr int F4_RING = (YOCO_TC_F4_RING / WK) & ~1023;
+    static constexpr int F4_STAGES = F4_RING / STAGE_BYTES;
     static constexpr int STAGES =
-        F8 ? (F8_STAGES < 2 ? 2 : F8_STAGES)
+        F4 ? (F4_STAGES > 6 ? 6 : F4_STAGES)
+        : F8 ? (F8_STAGES < 2 ? 2 : F8_STAGES)
            : (STAGE_BYTES == 16384 ? ((QSM || PR) ? 3 : YOCO_TC_ST16) : 3);
-    static constexpr int SUBE = 128 / ESZ;  // elements per 128-byte row of a sub-tile
-    static constexpr int KSUB = D / SUBE;   // 128-byte swizzled sub-tiles per row
-    static constexpr int SUB_BYTES = BS * 128;
+    // elements (bytes for e2m1) per row of a swizzled sub-tile: 128 bytes, or
+    // an e2m1 row's 64 at head_dim 128
+    static constexpr int SUBE = F4 ? ROW_BYTES : 128 / ESZ;
+    static constexpr int KSUB = F4 ? 1 : D / SUBE;  // sub-tiles per row
+    static constexpr int SUB_BYTES = F4 ? PAGE_BYTES : BS * 128;
     static constexpr int MT = BS / 16;   // 16-token tiles per page
     static constexpr int KD = D / 16;    // 16-wide steps along head_dim
     // Two 8-head tiles at head_dim 256 would hold the queries in 64 registers
@@ -121,10 +154,27 @@ struct TcShape {
     // segment sit in shared memory instead (16 rows x D, 16-bit), read per
     // page with ldmatrix.
     static constexpr int Q_BYTES = QSM ? 16 * D * 2 : 0;  // per warp
-    static constexpr int RING_BYTES = WK * STAGES * STAGE_BYTES;
-    static constexpr int SMEM = RING_BYTES + NW * Q_BYTES + 1024;
+    // a worker's part of the rings; e2m1 pages are small, so there its two
+    // end-of-slice pieces may take more than its stages
+    static constexpr int WBUF =
+        F4 && PIECE_PAIR > STAGES * STAGE_BYTES ? (PIECE_PAIR + 1023) & ~1023 : STAGES * STAGE_BYTES;
+    static constexpr int RING_BYTES = WK * WBUF;
+    // e2m1: every stage's scale record, and per warp the V multipliers of the
+    // page in hand (f16 [D / 32][BS])
+    static constexpr int F4_MUL = (D / 32) * BS * 2;
+    static constexpr int F4_BYTES = F4 ? WK * STAGES * F4_SREC + NW * F4_MUL : 0;
+    static constexpr int SMEM = RING_BYTES + NW * Q_BYTES + F4_BYTES + 1024;
     static_assert(SMEM <= 225 * 1024, "the rings must leave room for static shared memory");
 };
+
+// Byte offset of (token t, 16-byte chunk j) in an e2m1 page tile: rows of 64
+// bytes (64B swizzle) or 128 bytes (128B swizzle); either way the 8 rows an
+// ldmatrix reads fall in distinct banks.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t swz4(int t, int j) {
+    return static_cast<uint32_t>(
+        t * ROW_BYTES + ((j ^ (ROW_BYTES == 64 ? (t >> 1) & 3 : t & 7)) << 4));
+}
 
 // Byte offset of (token t, 16-byte chunk j of head-dim sub-tile c) in a
 // 128B-swizzled page tile.
@@ -740,13 +790,14 @@ __device__ __forceinline__ void cross_cta_merge(const AttnParams& p, const TcWs&
 // 2k + 1 columns 8-15. The pair's leader issues the copies; both wait on them
 // and agree on every outcome through one pair barrier, so that they always
 // take the same path.
-template <int D, int BS, int NT, bool REV, bool F8, bool FUSE, bool RG, bool PR>
-__global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
+template <int D, int BS, int NT, bool REV, int FMT, bool FUSE, bool RG, bool PR>
+__global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     attn_tc_persistent(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
-    using S = TcShape<D, BS, F8, NT, PR>;
+    using S = TcShape<D, BS, FMT, NT, PR>;
+    constexpr bool F8 = S::F8, F4 = S::F4;
     constexpr int NW = S::NW, WK = S::WK, STAGES = S::STAGES, NTG = S::NTG;
-    static_assert(S::PIECE_PAIR <= STAGES * S::STAGE_BYTES,
+    static_assert(S::PIECE_PAIR <= S::WBUF,
                   "a worker's two end-of-slice pieces must fit in its ring");
     static_assert(!F8 || D % 128 == 0, "e4m3 pages need 128-byte rows");
     static_assert(!RG || !FUSE, "the fused decode step has one row per request");
@@ -754,7 +805,9 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
     // the cross-CTA merge splits the CTA into two halves for its two segments,
     // each made of whole warps (its warp shuffles take full masks)
     static_assert(NW % 2 == 0, "an even number of warps per CTA");
-    static_assert(WK <= 15, "one named barrier per pair");
+    static_assert(!PR || WK <= 15, "one named barrier per pair");
+    static_assert(!F4 || (!FUSE && D % 128 == 0 && !S::QSM), "e2m1: whole 64-byte rows, no fused step");
+    static_assert(!F4 || (STAGES >= 2 && STAGES <= kPlanBlk), "e2m1 ring depth");
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[WK * STAGES];
     __shared__ int32_t stage_blk[WK * STAGES];  // physical page of each stage (-1: invalid)
@@ -773,7 +826,10 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
     const TcWs ws = tc_ws(p, gridDim.x, WK, D);
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint8_t* wbuf = smem + wk * STAGES * S::STAGE_BYTES;
+    uint8_t* wbuf = smem + wk * S::WBUF;
+    // e2m1: the worker's scale records, stage by stage, and this warp's V multipliers
+    uint8_t* const srec4 = smem + S::RING_BYTES + wk * STAGES * S::F4_SREC;
+    uint8_t* const vmul4 = smem + S::RING_BYTES + WK * STAGES * S::F4_SREC + warp * S::F4_MUL;
     uint64_t* wbar = bars + wk * STAGES;
     if (lane == 0 && leader) {  // each worker's ring barriers: only its warps wait on them
         for (int i = 0; i < STAGES; ++i) mbar_init(&wbar[i], 1);
@@ -874,7 +930,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
     // hint except the last keep_pages of this warp's walk (evict-last): about
     // kKeepBytes over the grid stay in L2 for the next layer, which walks the
     // other way and starts on them.
-    constexpr int64_t kKeepBytes = (F8 ? 20ll : 40ll) << 20;
+    constexpr int64_t kKeepBytes = (F8 || F4 ? 20ll : 40ll) << 20;
     const bool keep_tail = p.keep_tail != 0;
     const uint64_t pol_keep = keep_tail ? make_l2_policy_evict_last() : 0;
     const uint64_t pol_stream = keep_tail ? make_l2_policy_evict_first() : 0;
@@ -890,7 +946,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
             set_err(p.err, YOCO_DEVERR_PAGE_RANGE);
             mbar_arrive(bar);
         } else {
-            mbar_arrive_expect_tx(bar, 2 * S::PAGE_BYTES + (F8 ? 16 : 0));
+            mbar_arrive_expect_tx(bar, 2 * S::PAGE_BYTES + (F8 ? 16 : F4 ? S::F4_SREC : 0));
             uint8_t* kd = wbuf + st * S::STAGE_BYTES;
             uint8_t* vd = kd + S::PAGE_BYTES;
             const int32_t y = (blk * p.H_kv + pc.g) * BS;
@@ -911,6 +967,11 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
             if constexpr (F8)
                 bulk_load(&stage_scale[wk * STAGES + st],
                           p.scales + static_cast<int64_t>(blk) * p.H_kv + pc.g, 16, bar);
+            if constexpr (F4)
+                bulk_load(srec4 + st * S::F4_SREC,
+                          reinterpret_cast<const uint8_t*>(p.scales) +
+                              (static_cast<int64_t>(blk) * p.H_kv + pc.g) * S::F4_SREC,
+                          S::F4_SREC, bar);
         }
         step(pc);
     };
@@ -1012,8 +1073,19 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
     // segment's first page here, moved (and o rescaled) when a page's ratio
     // leaves [1/16, 16], so that the f16 weights stay in range
     float vref = 0.f, vinv = 0.f;
+    // e2m1: score factor of each column (with its query's power of two); the
+    // scale byte that the weights are taken against: o holds
+    // sum 2^8 p * 2^(b - vtop + 7) * code, vtop the largest V scale byte walked
+    // so far (never under 30), so that p down to 2^-22 and scales down to
+    // 2^-21 of the largest are whole f16 numbers. vref turns o into true units.
+    float qscale[NT][2];
+    int32_t vtop = 30;
     auto reset_state = [&]() {
         vref = 0.f;
+        if constexpr (F4) {
+            vtop = 30;
+            vref = __uint_as_float(static_cast<uint32_t>(30 - 7) << 23);
+        }
 #pragma unroll
         for (int a = 0; a < S::KD; ++a)
 #pragma unroll
@@ -1121,7 +1193,41 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                 }
                 const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) +
                                             ((static_cast<int64_t>(n) + hr) * p.H_q + g * p.G + hh) * D;
-                if constexpr (F8) {
+                if constexpr (F4) {
+                    // A lane's key registers hold 8 consecutive head dims 8tq.. of each 32:
+                    // the query takes the same order (16 bytes per 32 dims), as f16 after
+                    // the row's largest magnitude was brought to 2^14 by a power of two,
+                    // so that no magnitude of bf16 is out of range (elements 2^29 below
+                    // the largest lose bits); the score factor of its column undoes it.
+                    const uint4* src = reinterpret_cast<const uint4*>(qrow);
+                    uint4 v[D / 32];
+                    uint32_t mx = 0;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        v[c] = ok ? __ldg(src + c * 4 + tq) : make_uint4(0u, 0u, 0u, 0u);
+                        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                                   __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
+                    }
+                    mx = max(mx & 0xffffu, mx >> 16);
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const uint32_t f = max(mx >> 7, 20u);  // exponent field of the largest
+                    const float up = __uint_as_float((268u - f) << 23);
+                    const float down = __uint_as_float((f - 14u) << 23);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        qscale[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, down, (2 * tq + e) * 4);
+                    auto w = [up](uint32_t x) {
+                        return pack_f16x2(bf16lo_to_f32(x) * up, bf16hi_to_f32(x) * up);
+                    };
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        qf[2 * c][nt][0] = w(v[c].x);
+                        qf[2 * c][nt][1] = w(v[c].y);
+                        qf[2 * c + 1][nt][0] = w(v[c].z);
+                        qf[2 * c + 1][nt][1] = w(v[c].w);
+                    }
+                } else if constexpr (F8) {
                     const uint2* src = reinterpret_cast<const uint2*>(qrow);
 #pragma unroll
                     for (int kk = 0; kk < S::KD; ++kk) {
@@ -1161,7 +1267,9 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
     };
     // head dim of accumulator row gl (half 0) / gl + 8 (half 1) of 16-wide step md
     auto drow = [&](int md, int half) {
-        return F8 ? md * 16 + 2 * gl + half : md * 16 + gl + 8 * half;
+        return F4   ? (md >> 1) * 32 + 4 * gl + 2 * (md & 1) + half
+               : F8 ? md * 16 + 2 * gl + half
+                    : md * 16 + gl + 8 * half;
     };
     const float sl2 = p.scale_log2;
     bool aborted = false;
@@ -1212,6 +1320,42 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                     vr = 1.f;
                 }
             }
+            if constexpr (F4) {
+                // The page's V multipliers 2^(b - vtop + 7) as f16 (none for tokens past
+                // the causal end, whose bytes may be stale), laid out [32 dims][token] so
+                // that a lane's token pair is one word.
+                constexpr int GD = D / 32, NV = BS * GD / 32;  // scale bytes a lane takes
+                const uint8_t* sv = srec4 + st * S::F4_SREC + BS * GD;
+                int32_t b[NV], top = 0;
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {  // byte u * 32 + lane = token * GD + group
+                    const int x = u * 32 + lane;
+                    b[u] = x / GD < nvalid ? sv[x] : 0;
+                    top = max(top, b[u]);
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (top > vtop) {  // warp-uniform, rare
+                    const float f = top - vtop < 127
+                                        ? __uint_as_float(static_cast<uint32_t>(127 + vtop - top) << 23)
+                                        : 0.f;
+#pragma unroll
+                    for (int md = 0; md < S::KD; ++md)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[md][nt][c] *= f;
+                    vtop = top;
+                    vref = __uint_as_float(static_cast<uint32_t>(top - 7) << 23);
+                }
+                __syncwarp();  // the previous page's multipliers have been read
+#pragma unroll
+                for (int u = 0; u < NV; ++u) {
+                    const int x = u * 32 + lane;
+                    reinterpret_cast<uint16_t*>(vmul4)[(x % GD) * BS + x / GD] =
+                        static_cast<uint16_t>(max(b[u] - vtop + 22, 0) << 10);
+                }
+                __syncwarp();
+            }
             if (fused && cc.pp == (cc.kv_len - 1) / BS) {
                 // Fused decode step: the row's newest key is this step's token, which
                 // this launch also appends to the pools; whatever the page copy
@@ -1238,7 +1382,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                 fence_proxy_async_smem();  // before a later copy refills the stage
                 __syncwarp();
             }
-            if (nvalid < BS) {
+            if (!F4 && nvalid < BS) {
                 // Rows past the causal end may hold stale data (even NaN), and a
                 // zero probability times NaN is NaN: clear those V rows first.
                 // (a pair's warps clear alternate sub-tiles, then meet)
@@ -1254,7 +1398,55 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
             }
             // ---- S^T = K Q^T (tokens x heads); two accumulators halve the chain ----
             float sc[S::MT][NT][4];
-            {
+            if constexpr (F4) {
+                // One ldmatrix.x4 = 16 tokens x 64 head dims; a lane's 32-bit register holds
+                // 8 consecutive codes of one token, which widen to f16 exactly. Each 32
+                // dims' products (two k steps from zero) enter the score with their
+                // token's scale, so that no code is multiplied by it.
+                constexpr int GD = D / 32;
+                const int mi = lane >> 3, rr = lane & 7;
+                const uint8_t* sk = srec4 + st * S::F4_SREC;
+#pragma unroll
+                for (int mt = 0; mt < S::MT; ++mt) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sc[mt][nt][c] = 0.f;
+                    uint32_t w0[GD / 4], w1[GD / 4];  // scale bytes of tokens gl and gl + 8
+#pragma unroll
+                    for (int i = 0; i < GD / 4; ++i) {
+                        w0[i] = *reinterpret_cast<const uint32_t*>(sk + (mt * 16 + gl) * GD + 4 * i);
+                        w1[i] = *reinterpret_cast<const uint32_t*>(sk + (mt * 16 + gl + 8) * GD + 4 * i);
+                    }
+                    const int t = mt * 16 + (mi & 1) * 8 + rr;
+#pragma unroll
+                    for (int kp = 0; kp < GD / 2; ++kp) {
+                        uint32_t r[4];
+                        ldsm_x4(kbase + swz4<S::ROW_BYTES>(t, 2 * kp + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = 2 * kp + h;  // these 32 head dims
+                            uint32_t a[4], b[4];
+                            e2m1x8_to_f16x2(r[2 * h], a[0], a[1], a[2], a[3]);
+                            e2m1x8_to_f16x2(r[2 * h + 1], b[0], b[1], b[2], b[3]);
+                            const float s0 = scale_of_byte(w0[g >> 2], g & 3);
+                            const float s1 = scale_of_byte(w1[g >> 2], g & 3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float d[4];
+                                mma_f16_16816_zero(d, a[0], b[0], a[1], b[1], qf[2 * g][nt][0],
+                                                   qf[2 * g][nt][1]);
+                                mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * g + 1][nt][0],
+                                              qf[2 * g + 1][nt][1]);
+                                sc[mt][nt][0] = fmaf(d[0], s0, sc[mt][nt][0]);
+                                sc[mt][nt][1] = fmaf(d[1], s0, sc[mt][nt][1]);
+                                sc[mt][nt][2] = fmaf(d[2], s1, sc[mt][nt][2]);
+                                sc[mt][nt][3] = fmaf(d[3], s1, sc[mt][nt][3]);
+                            }
+                        }
+                    }
+                }
+            } else {
                 float sc2[S::MT][NT][4];
 #pragma unroll
                 for (int mt = 0; mt < S::MT; ++mt)
@@ -1418,8 +1610,8 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
                 }
-                const float mn0 = fmaxf(m_run[nt][0], mx0 * sl2p);
-                const float mn1 = fmaxf(m_run[nt][1], mx1 * sl2p);
+                const float mn0 = fmaxf(m_run[nt][0], mx0 * (F4 ? qscale[nt][0] : sl2p));
+                const float mn1 = fmaxf(m_run[nt][1], mx1 * (F4 ? qscale[nt][1] : sl2p));
                 // a column with no key yet (a group row whose keys all lie on later
                 // pages of a backward walk) keeps m = -inf: its weights and factor
                 // are taken against 0, so that they are 0 and never NaN
@@ -1445,7 +1637,56 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                 l_part[nt][1] *= corr[nt][1];
             }
             // ---- O^T += V^T P^T ----
-            if constexpr (F8) {
+            if constexpr (F4) {
+                uint32_t pb[S::MT][NT][2];  // 2^8 p in f16; the row sums take them unrounded
+#pragma unroll
+                for (int kt = 0; kt < S::MT; ++kt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float* c = sc[kt][nt];
+                        const float p0 = exp2_approx(fmaf(c[0], qscale[nt][0], 8.f - msafe[nt][0]));
+                        const float p1 = exp2_approx(fmaf(c[1], qscale[nt][1], 8.f - msafe[nt][1]));
+                        const float p2 = exp2_approx(fmaf(c[2], qscale[nt][0], 8.f - msafe[nt][0]));
+                        const float p3 = exp2_approx(fmaf(c[3], qscale[nt][1], 8.f - msafe[nt][1]));
+                        l_part[nt][0] += p0 + p2;
+                        l_part[nt][1] += p1 + p3;
+                        pb[kt][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                        pb[kt][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+                    }
+                // ldmatrix.trans over 16-bit units hands a lane head dims 4gl..4gl+3 of
+                // tokens 2tq (low half) and 2tq + 1 of each 32 dims: A-operand row gl
+                // takes dim 4gl (4gl + 2) and row gl + 8 dim 4gl + 1 (4gl + 3) of the 32
+                // dims' first (second) 16-row step. The weights, not the codes, take the
+                // token's scale: two products serve both steps.
+                constexpr int GD = D / 32;
+                const int mi = lane >> 3, rr = lane & 7;
+                const uint32_t* mul = reinterpret_cast<const uint32_t*>(vmul4) + tq;
+#pragma unroll
+                for (int mp = 0; mp < GD / 2; ++mp) {
+#pragma unroll
+                    for (int kt = 0; kt < S::MT; ++kt) {
+                        const int t = kt * 16 + (mi & 1) * 8 + rr;
+                        uint32_t r[4];
+                        ldsm_x4_trans(vbase + swz4<S::ROW_BYTES>(t, 2 * mp + (mi >> 1)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = 2 * mp + h;
+                            const uint32_t mlo = mul[g * (BS / 2) + kt * 8];
+                            const uint32_t mhi = mul[g * (BS / 2) + kt * 8 + 4];
+                            uint32_t x[4], y[4];  // dims 4gl + i of the lower / upper 8 tokens
+                            e2m1_pairs_to_f16x2(r[2 * h], x);
+                            e2m1_pairs_to_f16x2(r[2 * h + 1], y);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t b0 = mul_f16x2(pb[kt][nt][0], mlo);
+                                const uint32_t b1 = mul_f16x2(pb[kt][nt][1], mhi);
+                                mma_f16_16816(o[2 * g][nt], x[0], x[1], y[0], y[1], b0, b1);
+                                mma_f16_16816(o[2 * g + 1][nt], x[2], x[3], y[2], y[3], b0, b1);
+                            }
+                        }
+                    }
+                }
+            } else if constexpr (F8) {
                 // weights p * vr in f16 for all 16-token tiles; the row sums take p
                 uint32_t pb[S::MT][NT][2];
 #pragma unroll
@@ -1556,7 +1797,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                         // a group row without any key (seq_len below its request's rows)
                         // is zero-filled and flagged above: never written here
                         if (h >= nvh || (RG && l_part[nt][e] == 0.f)) continue;
-                        const float inv = (F8 ? vref : 1.f) / l_part[nt][e];
+                        const float inv = (F8 || F4 ? vref : 1.f) / l_part[nt][e];
                         const int hr = RG ? h / p.G : 0;
                         __nv_bfloat16* dst =
                             outp + ((static_cast<int64_t>(cc.n) + hr) * p.H_q + cc.g * p.G + (h - hr * p.G)) * D;
@@ -1591,7 +1832,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, F8, NT, PR>::NW * 32, 1)
                         const int h = c8 + nt * 8 + 2 * tq + e;
                         if (h >= nvh) continue;
                         float* dst = dst_o + h * D;
-                        const float of = F8 ? vref : 1.f;  // partials in true units
+                        const float of = F8 || F4 ? vref : 1.f;  // partials in true units
 #pragma unroll
                         for (int md = 0; md < S::KD; ++md) {
                             dst[drow(md, 0)] = o[md][nt][e] * of;
@@ -1785,16 +2026,16 @@ cudaError_t ensure_smem_attr(K kernel, int bytes, unsigned long long& done) {
 // Two-tile walks (groups over 8 heads, or rows grouped 16 wide) run as warp
 // pairs at these head dims, except the fused decode step (one warp per ring),
 // where a pair kernel has at most 8 warps (registers for the one-tile walk).
-template <int D, int BS, bool F8>
+template <int D, int BS, int FMT>
 constexpr bool tc_pairs() {
     return (D == 256 ? YOCO_TC_PAIRS256 != 0 : D == 128 ? YOCO_TC_PAIRS128 != 0 : false) &&
-           TcShape<D, BS, F8, 1, true>::NW <= 8;
+           (FMT == kE2m1 || TcShape<D, BS, FMT, 1, true>::NW <= 8);
 }
 
-template <int D, int BS, int NT, bool F8, bool PR>
+template <int D, int BS, int NT, int FMT, bool PR>
 cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int sms,
                        cudaStream_t s) {
-    using S = TcShape<D, BS, F8, NT, PR>;
+    using S = TcShape<D, BS, FMT, NT, PR>;
     static unsigned long long smem_fwd = 0, smem_rev = 0, smem_fuse = 0;  // one per kernel
     static unsigned long long smem_gfwd = 0, smem_grev = 0;
     const int ctas = tc_ctas(sms);
@@ -1830,20 +2071,26 @@ cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP
     // as warp pairs, a one-warp two-tile kernel serves the fused step alone.
     using K = void (*)(CUtensorMap, CUtensorMap, AttnParams);
     K kernel;
-    if constexpr (!PR && NT == 2 && tc_pairs<D, BS, F8>()) {
+    if constexpr (FMT == kE2m1) {  // no fused step over this cache
+        if (fuse) return cudaErrorInvalidConfiguration;
+        kernel = grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, true, PR>
+                                      : attn_tc_persistent<D, BS, NT, false, FMT, false, true, PR>)
+                         : (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, false, PR>
+                                      : attn_tc_persistent<D, BS, NT, false, FMT, false, false, PR>);
+    } else if constexpr (!PR && NT == 2 && tc_pairs<D, BS, FMT>()) {
         if (!fuse) return cudaErrorInvalidConfiguration;
-        kernel = attn_tc_persistent<D, BS, NT, false, F8, true, false, false>;
+        kernel = attn_tc_persistent<D, BS, NT, false, FMT, true, false, false>;
     } else if constexpr (PR) {
-        kernel = grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, F8, false, true, true>
-                                      : attn_tc_persistent<D, BS, NT, false, F8, false, true, true>)
-                         : (p.reverse ? attn_tc_persistent<D, BS, NT, true, F8, false, false, true>
-                                      : attn_tc_persistent<D, BS, NT, false, F8, false, false, true>);
+        kernel = grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, true, true>
+                                      : attn_tc_persistent<D, BS, NT, false, FMT, false, true, true>)
+                         : (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, false, true>
+                                      : attn_tc_persistent<D, BS, NT, false, FMT, false, false, true>);
     } else {
-        kernel = fuse ? attn_tc_persistent<D, BS, NT, false, F8, true, false, false>
-                 : grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, F8, false, true, false>
-                                        : attn_tc_persistent<D, BS, NT, false, F8, false, true, false>)
-                           : (p.reverse ? attn_tc_persistent<D, BS, NT, true, F8, false, false, false>
-                                        : attn_tc_persistent<D, BS, NT, false, F8, false, false, false>);
+        kernel = fuse ? attn_tc_persistent<D, BS, NT, false, FMT, true, false, false>
+                 : grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, true, false>
+                                        : attn_tc_persistent<D, BS, NT, false, FMT, false, true, false>)
+                           : (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, false, false>
+                                        : attn_tc_persistent<D, BS, NT, false, FMT, false, false, false>);
     }
     unsigned long long& done = fuse ? smem_fuse
                                : grouped ? (p.reverse ? smem_grev : smem_gfwd)
@@ -1860,21 +2107,24 @@ cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP
     return cudaLaunchKernelEx(&cfg, kernel, mk, mv, p);
 }
 
-template <int D, int BS, bool F8>
+template <int D, int BS, int FMT>
 cudaError_t launch_bs(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int sms,
                       cudaStream_t s) {
     const bool wide = p.vhs > 8;  // two 8-head tiles: a group over 8, or 16 virtual heads
-    if constexpr (tc_pairs<D, BS, F8>()) {
-        if (wide && p.k_new == nullptr) return launch_one<D, BS, 1, F8, true>(mk, mv, p, sms, s);
+    if constexpr (tc_pairs<D, BS, FMT>()) {
+        if (wide && p.k_new == nullptr) return launch_one<D, BS, 1, FMT, true>(mk, mv, p, sms, s);
     }
-    return wide ? launch_one<D, BS, 2, F8, false>(mk, mv, p, sms, s)
-                : launch_one<D, BS, 1, F8, false>(mk, mv, p, sms, s);
+    if constexpr (FMT == kE2m1 && tc_pairs<D, BS, FMT>())
+        return launch_one<D, BS, 1, FMT, false>(mk, mv, p, sms, s);
+    else
+        return wide ? launch_one<D, BS, 2, FMT, false>(mk, mv, p, sms, s)
+                    : launch_one<D, BS, 1, FMT, false>(mk, mv, p, sms, s);
 }
 
-template <int D, bool F8>
+template <int D, int FMT>
 cudaError_t launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int BS,
                      int sms, cudaStream_t s) {
-    return BS == 16 ? launch_bs<D, 16, F8>(mk, mv, p, sms, s) : launch_bs<D, 32, F8>(mk, mv, p, sms, s);
+    return BS == 16 ? launch_bs<D, 16, FMT>(mk, mv, p, sms, s) : launch_bs<D, 32, FMT>(mk, mv, p, sms, s);
 }
 
 }  // namespace

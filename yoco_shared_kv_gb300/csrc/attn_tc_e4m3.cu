@@ -7,8 +7,8 @@ namespace yoco {
 
 cudaError_t launch_attn_tc_e4m3(const CUtensorMap& mk, const CUtensorMap& mv,
                                 const AttnParams& p, int D, int BS, int sms, cudaStream_t s) {
-    if (D == 128) return launch_d<128, true>(mk, mv, p, BS, sms, s);
-    return launch_d<256, true>(mk, mv, p, BS, sms, s);
+    if (D == 128) return launch_d<128, kE4m3>(mk, mv, p, BS, sms, s);
+    return launch_d<256, kE4m3>(mk, mv, p, BS, sms, s);
 }
 
 }  // namespace yoco

@@ -2,7 +2,8 @@
 // plan of the fp32 path, the pools' TMA descriptors and the launch.
 //
 // bf16 runs on the persistent tensor-core path (attn_tc.cu), an e4m3 cache
-// on the same path with one-byte pages (attn_tc_e4m3.cu); fp32 runs on the
+// on the same path with one-byte pages (attn_tc_e4m3.cu), an e2m1 cache with
+// half-byte pages (attn_tc_e2m1.cu); fp32 runs on the
 // CUDA-core split-KV path (attn_cc.cu).
 #include <mutex>
 
@@ -23,19 +24,20 @@ struct Plan {
 
 bool make_plan(yoco_dtype_t dt, int max_rows, int H_q, int H_kv, int D, int BS, int max_seq_len,
                Plan& pl) {
-    const bool e4m3 = dt == YOCO_E4M3;
-    if (!(dtype_ok(dt) || e4m3) || !head_dim_ok(D) || !block_size_ok(BS)) return false;
-    if (e4m3 && D == 64) return false;  // e4m3 pages need 128-byte rows
+    const bool e4m3 = dt == YOCO_E4M3, e2m1 = dt == YOCO_E2M1;
+    if (!(dtype_ok(dt) || e4m3 || e2m1) || !head_dim_ok(D) || !block_size_ok(BS)) return false;
+    if ((e4m3 || e2m1) && D == 64) return false;  // quantised pages need wider rows
     if (H_q <= 0 || H_kv <= 0 || H_q % H_kv != 0 || H_q / H_kv > 16) return false;
     if (max_rows < 0 || max_seq_len <= 0) return false;
     const int G = H_q / H_kv;
     const int sms = device_sm_count();
-    pl.tc = (dt == YOCO_BF16 || e4m3);
+    pl.tc = (dt == YOCO_BF16 || e4m3 || e2m1);
     pl.hb = 1;
     pl.split_pages = 0;
     pl.max_splits = 1;
     if (pl.tc) {
-        pl.ws_bytes = tc_workspace_bytes(sms, H_kv, G, D, BS, e4m3);
+        pl.ws_bytes = tc_workspace_bytes(sms, H_kv, G, D, BS,
+                                         e4m3 ? kE4m3 : e2m1 ? kE2m1 : kBf16);
         return true;
     }
     for (int c : {8, 4, 2, 1})
@@ -82,18 +84,22 @@ EncodeTiledFn encode_fn() {
 }
 
 // Pool [num_blocks * H_kv * BS rows][D] as a 2-D tensor of bf16 (esz 2) or
-// bytes (esz 1); box = 128 bytes x BS rows with the 128-byte swizzle.
+// bytes (esz 1); box = 128 bytes x BS rows with the 128-byte swizzle, or whole
+// 64-byte rows with the 64-byte swizzle (e2m1 at head_dim 128).
 bool encode_pool(CUtensorMap* map, const void* pool, int64_t rows, int D, int BS, int esz) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * esz};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(BS)};
+    const bool narrow = D * esz == 64;
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(narrow ? D : 128 / esz),
+                               static_cast<cuuint32_t>(BS)};
     const cuuint32_t estr[2] = {1, 1};
     const CUtensorMapDataType ty =
         esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return fn(map, ty, 2, const_cast<void*>(pool), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -161,10 +167,10 @@ extern "C" size_t yoco_cross_attn_workspace_size(int32_t max_rows, int32_t num_q
 namespace yoco {
 namespace {
 
-// Shared body of the attention entry points; dtype YOCO_E4M3 = bf16 queries
-// over an e4m3 cache with its scale records.
+// Shared body of the attention entry points; dtype YOCO_E4M3 (YOCO_E2M1) =
+// bf16 queries over an e4m3 (e2m1) cache with its scale records (bytes).
 yoco_status_t run_attn(const void* q, const void* k_cache, const void* v_cache,
-                       const float* page_scales, void* out, const int32_t* block_table,
+                       const void* page_scales, void* out, const int32_t* block_table,
                        int32_t max_blocks_per_req, const int32_t* seq_lens,
                        const int32_t* cross_query_start_loc, int32_t num_reqs, int32_t max_rows,
                        int32_t max_seq_len, int32_t num_q_heads, int32_t num_kv_heads,
@@ -173,12 +179,12 @@ yoco_status_t run_attn(const void* q, const void* k_cache, const void* v_cache,
                        size_t workspace_bytes, int32_t* err_word, void* stream,
                        const void* k_new = nullptr, const void* v_new = nullptr,
                        bool plan_only = false) {
-    const bool e4m3 = dtype == YOCO_E4M3;
+    const bool e4m3 = dtype == YOCO_E4M3, e2m1 = dtype == YOCO_E2M1;
     if (flags & ~static_cast<uint32_t>(YOCO_ATTN_REVERSE | YOCO_ATTN_OVERLAP |
                                        YOCO_ATTN_KEEP_TAIL | YOCO_ATTN_PLANNED))
         return YOCO_ERR_INVALID_ARG;
-    if (!(dtype_ok(dtype) || e4m3) || !head_dim_ok(head_dim) || !block_size_ok(block_size) ||
-        (e4m3 && head_dim == 64))
+    if (!(dtype_ok(dtype) || e4m3 || e2m1) || !head_dim_ok(head_dim) ||
+        !block_size_ok(block_size) || ((e4m3 || e2m1) && head_dim == 64))
         return YOCO_ERR_UNSUPPORTED;
     if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
         return YOCO_ERR_INVALID_ARG;
@@ -190,7 +196,7 @@ yoco_status_t run_attn(const void* q, const void* k_cache, const void* v_cache,
     if (!block_table || !seq_lens || !cross_query_start_loc) return YOCO_ERR_INVALID_ARG;
     if (!plan_only) {
         if (!q || !k_cache || !v_cache || !out) return YOCO_ERR_INVALID_ARG;
-        if (e4m3 && (page_scales == nullptr || !aligned16(page_scales)))
+        if ((e4m3 || e2m1) && (page_scales == nullptr || !aligned16(page_scales)))
             return YOCO_ERR_INVALID_ARG;
         if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
             return YOCO_ERR_INVALID_ARG;
@@ -229,7 +235,7 @@ yoco_status_t run_attn(const void* q, const void* k_cache, const void* v_cache,
     p.split_pages = pl.split_pages;
     p.max_splits = pl.max_splits;
     p.max_seq_len = max_seq_len;
-    p.scales = reinterpret_cast<const float4*>(page_scales);
+    p.scales = static_cast<const float4*>(page_scales);
     p.scale_log2 = scale * kLog2e;
     p.reverse = (flags & YOCO_ATTN_REVERSE) ? 1 : 0;
     p.overlap = (flags & YOCO_ATTN_OVERLAP) ? 1 : 0;
@@ -265,12 +271,13 @@ yoco_status_t run_attn(const void* q, const void* k_cache, const void* v_cache,
         p.ws_ml = nullptr;
         CUtensorMap mk = {}, mv = {};
         const int64_t rows = static_cast<int64_t>(num_blocks) * num_kv_heads * block_size;
-        const int esz = e4m3 ? 1 : 2;
-        if (!plan_only && (!pool_map(&mk, k_cache, rows, head_dim, block_size, esz) ||
-                           !pool_map(&mv, v_cache, rows, head_dim, block_size, esz)))
+        const int esz = e4m3 || e2m1 ? 1 : 2, row = e2m1 ? head_dim / 2 : head_dim;
+        if (!plan_only && (!pool_map(&mk, k_cache, rows, row, block_size, esz) ||
+                           !pool_map(&mv, v_cache, rows, row, block_size, esz)))
             return cuda_status(cudaErrorInvalidValue);  // descriptor encoding refused
-        e = e4m3 ? launch_attn_tc_e4m3(mk, mv, p, head_dim, block_size, device_sm_count(), s)
-                 : launch_attn_tc(mk, mv, p, head_dim, block_size, device_sm_count(), s);
+        e = e2m1   ? launch_attn_tc_e2m1(mk, mv, p, head_dim, block_size, device_sm_count(), s)
+            : e4m3 ? launch_attn_tc_e4m3(mk, mv, p, head_dim, block_size, device_sm_count(), s)
+                   : launch_attn_tc(mk, mv, p, head_dim, block_size, device_sm_count(), s);
     } else {
         p.ws_o = static_cast<float*>(workspace);
         p.ws_ml = pl.max_splits > 1
@@ -293,7 +300,8 @@ extern "C" yoco_status_t yoco_cross_attn_paged(
     int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, float scale,
     yoco_dtype_t dtype, uint32_t flags, void* workspace, size_t workspace_bytes, int32_t* err_word,
     void* stream) {
-    if (dtype == YOCO_E4M3) return YOCO_ERR_UNSUPPORTED;  // the e4m3 cache has its own entry
+    if (dtype == YOCO_E4M3 || dtype == YOCO_E2M1)
+        return YOCO_ERR_UNSUPPORTED;  // the quantised caches have their own entries
     return yoco::run_attn(q, k_cache, v_cache, nullptr, out, block_table, max_blocks_per_req,
                           seq_lens, cross_query_start_loc, num_reqs, max_rows, max_seq_len,
                           num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
@@ -325,6 +333,19 @@ extern "C" yoco_status_t yoco_cross_attn_paged_e4m3(
                           seq_lens, cross_query_start_loc, num_reqs, max_rows, max_seq_len,
                           num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                           YOCO_E4M3, flags, workspace, workspace_bytes, err_word, stream);
+}
+
+extern "C" yoco_status_t yoco_cross_attn_paged_e2m1(
+    const void* q, const void* k_cache, const void* v_cache, const void* block_scales, void* out,
+    const int32_t* block_table, int32_t max_blocks_per_req, const int32_t* seq_lens,
+    const int32_t* cross_query_start_loc, int32_t num_reqs, int32_t max_rows, int32_t max_seq_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+    int32_t num_blocks, float scale, uint32_t flags, void* workspace, size_t workspace_bytes,
+    int32_t* err_word, void* stream) {
+    return yoco::run_attn(q, k_cache, v_cache, block_scales, out, block_table, max_blocks_per_req,
+                          seq_lens, cross_query_start_loc, num_reqs, max_rows, max_seq_len,
+                          num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                          YOCO_E2M1, flags, workspace, workspace_bytes, err_word, stream);
 }
 
 extern "C" yoco_status_t yoco_cross_decode_step(
