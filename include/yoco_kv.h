@@ -89,6 +89,7 @@ typedef enum { YOCO_F32 = 0, YOCO_BF16 = 1, YOCO_E4M3 = 2, YOCO_E2M1 = 3 } yoco_
 #define YOCO_DEVERR_SCALE 0x20       /* e4m3 cache: a page scale outside the supported range */
 #define YOCO_DEVERR_PLAN 0x40        /* YOCO_ATTN_PLANNED, but the workspace holds no plan for these shapes */
 #define YOCO_DEVERR_NO_PAGES 0x80    /* yoco_build_block_tables: the free pages do not cover the step */
+#define YOCO_DEVERR_STATE 0x100      /* yoco_retention: a state index outside [0, num_states) */
 
 /*
  * yoco_kv_append — write the step's new shared K^/V^ into the paged cache.
@@ -447,6 +448,55 @@ yoco_status_t yoco_cross_attn_paged_e2m1(const void* q, const void* k_cache, con
                                          int32_t head_dim, int32_t block_size, int32_t num_blocks,
                                          float scale, uint32_t flags, void* workspace,
                                          size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/*
+ * yoco_retention — linear attention with a decay per head: the self-decoder's
+ * gated retention, for prompts in chunks and for single tokens recurrently.
+ *
+ * "YOCO 论文与推理数据流详解" §4.1-§4.2: the self-decoder keeps one state of
+ * constant size per head instead of a cache, S_t = a_t S_(t-1) + k_t v_t^T,
+ * with a_t = exp(g_t) given by token (gated) or by head (fixed), and answers
+ *   o_t = scale * q_t^T S_t.
+ * The tokens of request r are query_start_loc[r] .. query_start_loc[r + 1] - 1;
+ * they continue the state of the tokens before them, or start from zero when
+ * seq_lens[r] equals their number (that state is then not read).
+ *   q, out         device bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned; rows from
+ *                  query_start_loc[num_reqs] on are neither read nor written
+ *   k, v           device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte aligned; head h
+ *                  reads k/v head h / (num_q_heads / num_kv_heads)
+ *   log_decay      device float32 g, [num_tokens][num_q_heads] with decay_per_token, else
+ *                  [num_q_heads]; at most 0 for a decay. Below -80 counts as -80 (exp = 2e-35)
+ *   state          device float32 [num_states][num_q_heads][head_dim (k)][head_dim (v)]
+ *   state_out      the states after the call, in the same layout; may be `state` itself.
+ *                  States of no request with tokens are not touched
+ *   state_indices  device int32 [num_reqs]: request r's state; distinct for requests with tokens
+ *   seq_lens       device int32 [num_reqs]: tokens of the sequence after this step
+ *   max_q_len      host bound on the tokens of a request (1: every request is a single token,
+ *                  and the call is one launch)
+ *   workspace      device, >= yoco_retention_workspace_size(...) bytes, 16-byte aligned; may be
+ *                  NULL where that is 0. One workspace serves one stream at a time
+ *   err_word       device int32 or NULL
+ * A request with malformed offsets, or more tokens than max_q_len, sets
+ * YOCO_DEVERR_OFFSETS, one with seq_len < its tokens YOCO_DEVERR_POS_RANGE,
+ * one with a state outside [0, num_states) YOCO_DEVERR_STATE; its rows of out
+ * and its state are left as they were. head_dim 64, 128 or 256. The state and
+ * every sum are fp32; outputs of prompts round the weights of a chunk and the
+ * state's copy that multiplies q to bf16; the state after the step takes the
+ * decayed values in 24 bits. Results do not depend on timing.
+ */
+yoco_status_t yoco_retention(const void* q, const void* k, const void* v, const float* log_decay,
+                             int32_t decay_per_token, const float* state, float* state_out,
+                             const int32_t* state_indices, void* out,
+                             const int32_t* query_start_loc, const int32_t* seq_lens,
+                             int32_t num_reqs, int32_t num_tokens, int32_t max_q_len,
+                             int32_t num_states, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, float scale, void* workspace,
+                             size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/* Bytes of scratch yoco_retention needs for up to these bounds on the current
+ * device (0 for single tokens, and for invalid arguments). */
+size_t yoco_retention_workspace_size(int32_t num_reqs, int32_t num_tokens, int32_t max_q_len,
+                                     int32_t num_q_heads, int32_t head_dim);
 
 /*
  * yoco_cross_decode_step — a decode step's append and its first cross-decoder

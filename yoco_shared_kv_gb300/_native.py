@@ -32,6 +32,7 @@ DEVERR_TIMEOUT = 0x10
 DEVERR_SCALE = 0x20
 DEVERR_PLAN = 0x40
 DEVERR_NO_PAGES = 0x80
+DEVERR_STATE = 0x100
 
 EXPORTED = ("yoco_kv_append", "yoco_select_cross_rows", "yoco_cross_attn_workspace_size",
             "yoco_cross_attn_paged", "yoco_set_l2_window", "yoco_status_string", "yoco_version",
@@ -40,7 +41,7 @@ EXPORTED = ("yoco_kv_append", "yoco_select_cross_rows", "yoco_cross_attn_workspa
             "yoco_selftest_wait_timeout", "yoco_cross_decoder_bytes", "yoco_kv_append_e4m3",
             "yoco_cross_attn_paged_e4m3", "yoco_cross_decode_step", "yoco_cross_attn_plan",
             "yoco_build_block_tables", "yoco_kv_append_e2m1", "yoco_kv_gather_e2m1",
-            "yoco_cross_attn_paged_e2m1")
+            "yoco_cross_attn_paged_e2m1", "yoco_retention", "yoco_retention_workspace_size")
 
 
 class YocoError(RuntimeError):
@@ -115,6 +116,11 @@ def _load() -> ctypes.CDLL:
     L.yoco_cross_attn_paged_e2m1.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32,
                                              i32, i32, i32, i32, i32, ctypes.c_float,
                                              ctypes.c_uint32, vp, sz, vp, vp]
+    L.yoco_retention.restype = ctypes.c_int
+    L.yoco_retention.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                 i32, i32, i32, ctypes.c_float, vp, sz, vp, vp]
+    L.yoco_retention_workspace_size.restype = sz
+    L.yoco_retention_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     return L
 
 
@@ -482,3 +488,36 @@ def yoco_cross_attn_paged_e2m1(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         int(max_seq_len), H_q, H_kv, D, bs, num_blocks, float(scale), int(flags),
         _arg(workspace, torch.uint8, (ws_bytes,), "workspace"), ws_bytes,
         _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+
+
+def yoco_retention_workspace_size(num_reqs: int, num_tokens: int, max_q_len: int, num_q_heads: int,
+                                  head_dim: int) -> int:
+    return int(lib.yoco_retention_workspace_size(num_reqs, num_tokens, max_q_len, num_q_heads,
+                                                 head_dim))
+
+
+def yoco_retention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                   state: torch.Tensor, state_indices: torch.Tensor, out: torch.Tensor,
+                   query_start_loc: torch.Tensor, seq_lens: torch.Tensor, max_q_len: int,
+                   scale: float, workspace: Optional[torch.Tensor] = None,
+                   state_out: Optional[torch.Tensor] = None,
+                   err_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Linear attention with decay: bf16 ``q/out [T, H, D]``, ``k/v [T, H_kv, D]``, float32
+    ``log_decay [H]`` or ``[T, H]``, states ``[num_states, H, D, D]`` (``state_out`` None: in place)."""
+    T, H, D = q.shape
+    H_kv = k.shape[1]
+    R = seq_lens.numel()
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    num_states = state.shape[0]
+    by_token = log_decay.dim() == 2
+    ws_bytes = 0 if workspace is None else workspace.numel()
+    st = _arg(state, f32, (num_states, H, D, D), "state")
+    _check("yoco_retention", lib.yoco_retention(
+        _arg(q, bf, (T, H, D), "q"), _arg(k, bf, (T, H_kv, D), "k"), _arg(v, bf, (T, H_kv, D), "v"),
+        _arg(log_decay, f32, (T, H) if by_token else (H,), "log_decay"), int(by_token), st,
+        st if state_out is None else _arg(state_out, f32, (num_states, H, D, D), "state_out"),
+        _arg(state_indices, i32, (R,), "state_indices"), _arg(out, bf, (T, H, D), "out"),
+        _arg(query_start_loc, i32, (R + 1,), "query_start_loc"), _arg(seq_lens, i32, (R,), "seq_lens"),
+        R, T, int(max_q_len), num_states, H, H_kv, D, float(scale),
+        _arg(workspace, torch.uint8, (ws_bytes,), "workspace"), ws_bytes,
+        _arg(err_word, i32, (1,), "err_word"), _stream(stream)))

@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libyoco_kv.so")
 SOURCES = ["abi.cu", "kv_append.cu", "select_rows.cu", "cross_attn.cu", "attn_tc.cu",
            "attn_tc_e4m3.cu", "attn_tc_e2m1.cu", "attn_cc.cu", "attn_static.cu", "block_tables.cu",
-           "kv_e2m1.cu"]
+           "kv_e2m1.cu", "retention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}"]
