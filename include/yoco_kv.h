@@ -434,7 +434,7 @@ yoco_status_t yoco_kv_gather_e2m1(const void* k_cache, const void* v_cache,
  * codes widen exactly to f16; each query head is brought into f16's range by
  * a power of two and is exact there but for elements 2^29 below its largest;
  * products and sums in fp32, a block's sum taking its K scale in fp32;
- * softmax weights round to f16 (under 2^-32 of the largest they are gone), and
+ * softmax weights round to f16 (under 2^-28 of the largest they are gone), and
  * V scales more than 2^21 below the largest that a walk has met count for nothing. Everything else (flags,
  * errors, determinism) is as for yoco_cross_attn_paged.
  */

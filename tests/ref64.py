@@ -101,11 +101,12 @@ def cross_attn_e2m1(q, k_cache, v_cache, scales, table, seq_lens, cqsl, scale, m
     or sum 2^-24 of the magnitudes summed, D + 64 of them, then exp).
 
     f16 has an absolute step below 2^-14, half of it 2^-25, which a relative
-    step does not count. The weights are held as 2^8 p, so each is off by up
-    to 2^-33 as well: 2^-33 of sum |v|. Times its token's scale over the
-    largest scale times 2^7 it may fall below 2^-14 once more: off by 2^-25 in
-    units of 2^(top - 127 - 15), that is 2^-40 of the largest scale, for each
-    of the keys with codes up to 6.
+    step does not count. The weights are held as 2^3 p or more (relative to a
+    reference at most the largest score), so each is off by up to 2^-28 as
+    well: 2^-28 of sum |v|. Times its token's scale over the largest scale
+    times 2^7 it may fall below 2^-14 once more: off by 2^-25 in units of
+    2^(top - 127 - 10), that is 2^-35 of the largest scale, for each of the
+    keys with codes up to 6.
     """
     rows = min(int(cqsl[-1]), max_rows)
     H_q, D = q.shape[1:]
@@ -136,7 +137,7 @@ def cross_attn_e2m1(q, k_cache, v_cache, scales, table, seq_lens, cqsl, scale, m
                 out[row, at] = o
                 tol[row, at] = 2.0 ** -8 * np.abs(o) + (2.0 ** -11 + 2.2 * ds) * (p @ np.abs(v[:keys]))
                 top = np.ldexp(1.0, int(scales[pages, h, 1].reshape(-1, D // 32)[:keys].max()) - 127)
-                tol[row, at] += 2.0 ** -33 * np.abs(v[:keys]).sum(0) + 2.0 ** -40 * 6 * keys * top + 1e-30
+                tol[row, at] += 2.0 ** -28 * np.abs(v[:keys]).sum(0) + 2.0 ** -35 * 6 * keys * top + 1e-30
     return out, tol
 
 

@@ -168,6 +168,8 @@ def _i32(t: torch.Tensor, name: str) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized():  # the handle itself, without a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -392,17 +394,30 @@ def yoco_cross_decode_step(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Te
 
 
 
-def _arg(t: Optional[torch.Tensor], dtype: torch.dtype, shape, name: str) -> Optional[int]:
-    """Pointer of a contiguous tensor of this dtype and shape on the current device."""
+# Host time is most of a small call's time: the wrappers below look at each tensor
+# once and take device and raw stream from the calls that torch's own wrappers make.
+
+
+def _current(stream):
+    """(current device, stream handle); no device (and no CUDA tensor) before CUDA starts."""
+    if not torch.cuda.is_initialized():
+        return -2, None
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _arg(t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, name: str,
+         dev: int) -> Optional[int]:
+    """Pointer of a contiguous tensor of this dtype and shape on device ``dev``."""
     if t is None:
         return None
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}: got {t.dtype} {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on the current CUDA device: it is on {t.device}")
 
 
 def yoco_build_block_tables(block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -413,26 +428,27 @@ def yoco_build_block_tables(block_table: torch.Tensor, seq_lens: torch.Tensor,
                             err_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Extend ``block_table [R, max_blocks]`` by the pages the step's tokens need (from the
     stack ``free_pages[:num_free]``, or none when it is None) and fill ``slot_mapping [T]``."""
+    dev, strm = _current(stream)
     i32 = torch.int32
     R, max_blocks = block_table.shape
     T = slot_mapping.numel()
     cap = 0 if free_pages is None else free_pages.numel()
     _check("yoco_build_block_tables", lib.yoco_build_block_tables(
-        _arg(block_table, i32, (R, max_blocks), "block_table"), max_blocks,
-        _arg(seq_lens, i32, (R,), "seq_lens"), _arg(query_start_loc, i32, (R + 1,), "query_start_loc"),
-        R, T, int(num_blocks), int(block_size), _arg(free_pages, i32, (cap,), "free_pages"), cap,
-        _arg(num_free, i32, (1,), "num_free"), _arg(num_free_after, i32, (1,), "num_free_after"),
-        _arg(slot_mapping, i32, (T,), "slot_mapping"), _arg(err_word, i32, (1,), "err_word"),
-        _stream(stream)))
+        _arg(block_table, i32, (R, max_blocks), "block_table", dev), max_blocks,
+        _arg(seq_lens, i32, (R,), "seq_lens", dev), _arg(query_start_loc, i32, (R + 1,), "query_start_loc", dev),
+        R, T, int(num_blocks), int(block_size), _arg(free_pages, i32, (cap,), "free_pages", dev), cap,
+        _arg(num_free, i32, (1,), "num_free", dev), _arg(num_free_after, i32, (1,), "num_free_after", dev),
+        _arg(slot_mapping, i32, (T,), "slot_mapping", dev), _arg(err_word, i32, (1,), "err_word", dev),
+        strm))
 
 
-def _e2m1_pools(k_cache: torch.Tensor, v_cache: torch.Tensor, block_scales: torch.Tensor):
+def _e2m1_pools(k_cache: torch.Tensor, v_cache: torch.Tensor, block_scales: torch.Tensor, dev: int):
     """(pointers, num_blocks, H_kv, block_size, D) of a 4-bit cache."""
     u8 = torch.uint8
     num_blocks, H_kv, bs, half = k_cache.shape
     shape = (num_blocks, H_kv, bs, half)
-    ptrs = (_arg(k_cache, u8, shape, "k_cache"), _arg(v_cache, u8, shape, "v_cache"),
-            _arg(block_scales, u8, (num_blocks, H_kv, 2, bs, half // 16), "block_scales"))
+    ptrs = (_arg(k_cache, u8, shape, "k_cache", dev), _arg(v_cache, u8, shape, "v_cache", dev),
+            _arg(block_scales, u8, (num_blocks, H_kv, 2, bs, half // 16), "block_scales", dev))
     return ptrs, num_blocks, H_kv, bs, 2 * half
 
 
@@ -442,26 +458,28 @@ def yoco_kv_append_e2m1(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch
                         stream=None) -> None:
     """Quantising append: bf16 ``k_new/v_new [T, H_kv, D]`` into 4-bit pools
     ``[num_blocks, H_kv, bs, D / 2]`` with scale bytes ``[num_blocks, H_kv, 2, bs, D / 32]``."""
-    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    dev, strm = _current(stream)
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales, dev)
     T = slot_mapping.numel()
     _check("yoco_kv_append_e2m1", lib.yoco_kv_append_e2m1(
-        _arg(k_new, torch.bfloat16, (T, H_kv, D), "k_new"),
-        _arg(v_new, torch.bfloat16, (T, H_kv, D), "v_new"), *pools,
-        _arg(slot_mapping, torch.int32, (T,), "slot_mapping"), T, num_blocks, bs, H_kv, D,
-        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+        _arg(k_new, torch.bfloat16, (T, H_kv, D), "k_new", dev),
+        _arg(v_new, torch.bfloat16, (T, H_kv, D), "v_new", dev), *pools,
+        _arg(slot_mapping, torch.int32, (T,), "slot_mapping", dev), T, num_blocks, bs, H_kv, D,
+        _arg(err_word, torch.int32, (1,), "err_word", dev), strm))
 
 
 def yoco_kv_gather_e2m1(k_cache: torch.Tensor, v_cache: torch.Tensor, block_scales: torch.Tensor,
                         slot_mapping: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
                         err_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows of a 4-bit cache as the bf16 values they stand for: ``k_out/v_out [T, H_kv, D]``."""
-    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    dev, strm = _current(stream)
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales, dev)
     T = slot_mapping.numel()
     _check("yoco_kv_gather_e2m1", lib.yoco_kv_gather_e2m1(
-        *pools, _arg(slot_mapping, torch.int32, (T,), "slot_mapping"),
-        _arg(k_out, torch.bfloat16, (T, H_kv, D), "k_out"),
-        _arg(v_out, torch.bfloat16, (T, H_kv, D), "v_out"), T, num_blocks, bs, H_kv, D,
-        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+        *pools, _arg(slot_mapping, torch.int32, (T,), "slot_mapping", dev),
+        _arg(k_out, torch.bfloat16, (T, H_kv, D), "k_out", dev),
+        _arg(v_out, torch.bfloat16, (T, H_kv, D), "v_out", dev), T, num_blocks, bs, H_kv, D,
+        _arg(err_word, torch.int32, (1,), "err_word", dev), strm))
 
 
 def yoco_cross_attn_paged_e2m1(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -472,7 +490,8 @@ def yoco_cross_attn_paged_e2m1(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                err_word: Optional[torch.Tensor] = None, stream=None,
                                max_rows: Optional[int] = None, flags: int = 0) -> None:
     """One layer over a 4-bit cache: bf16 ``q/out [max_rows, H_q, D]``."""
-    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales)
+    dev, strm = _current(stream)
+    pools, num_blocks, H_kv, bs, D = _e2m1_pools(k_cache, v_cache, block_scales, dev)
     rows_cap, H_q = q.shape[:2]
     R, max_blocks = block_table.shape
     max_rows = rows_cap if max_rows is None else int(max_rows)
@@ -480,14 +499,14 @@ def yoco_cross_attn_paged_e2m1(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         raise ValueError("max_rows is more than q holds")
     ws_bytes = 0 if workspace is None else workspace.numel()
     _check("yoco_cross_attn_paged_e2m1", lib.yoco_cross_attn_paged_e2m1(
-        _arg(q, torch.bfloat16, (rows_cap, H_q, D), "q"), *pools,
-        _arg(out, torch.bfloat16, (rows_cap, H_q, D), "out"),
-        _arg(block_table, torch.int32, (R, max_blocks), "block_table"), max_blocks,
-        _arg(seq_lens, torch.int32, (R,), "seq_lens"),
-        _arg(cross_query_start_loc, torch.int32, (R + 1,), "cross_query_start_loc"), R, max_rows,
+        _arg(q, torch.bfloat16, (rows_cap, H_q, D), "q", dev), *pools,
+        _arg(out, torch.bfloat16, (rows_cap, H_q, D), "out", dev),
+        _arg(block_table, torch.int32, (R, max_blocks), "block_table", dev), max_blocks,
+        _arg(seq_lens, torch.int32, (R,), "seq_lens", dev),
+        _arg(cross_query_start_loc, torch.int32, (R + 1,), "cross_query_start_loc", dev), R, max_rows,
         int(max_seq_len), H_q, H_kv, D, bs, num_blocks, float(scale), int(flags),
-        _arg(workspace, torch.uint8, (ws_bytes,), "workspace"), ws_bytes,
-        _arg(err_word, torch.int32, (1,), "err_word"), _stream(stream)))
+        _arg(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes,
+        _arg(err_word, torch.int32, (1,), "err_word", dev), strm))
 
 
 def yoco_retention_workspace_size(num_reqs: int, num_tokens: int, max_q_len: int, num_q_heads: int,
@@ -504,6 +523,7 @@ def yoco_retention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay:
                    err_word: Optional[torch.Tensor] = None, stream=None) -> None:
     """Linear attention with decay: bf16 ``q/out [T, H, D]``, ``k/v [T, H_kv, D]``, float32
     ``log_decay [H]`` or ``[T, H]``, states ``[num_states, H, D, D]`` (``state_out`` None: in place)."""
+    dev, strm = _current(stream)
     T, H, D = q.shape
     H_kv = k.shape[1]
     R = seq_lens.numel()
@@ -511,13 +531,13 @@ def yoco_retention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay:
     num_states = state.shape[0]
     by_token = log_decay.dim() == 2
     ws_bytes = 0 if workspace is None else workspace.numel()
-    st = _arg(state, f32, (num_states, H, D, D), "state")
+    st = _arg(state, f32, (num_states, H, D, D), "state", dev)
     _check("yoco_retention", lib.yoco_retention(
-        _arg(q, bf, (T, H, D), "q"), _arg(k, bf, (T, H_kv, D), "k"), _arg(v, bf, (T, H_kv, D), "v"),
-        _arg(log_decay, f32, (T, H) if by_token else (H,), "log_decay"), int(by_token), st,
-        st if state_out is None else _arg(state_out, f32, (num_states, H, D, D), "state_out"),
-        _arg(state_indices, i32, (R,), "state_indices"), _arg(out, bf, (T, H, D), "out"),
-        _arg(query_start_loc, i32, (R + 1,), "query_start_loc"), _arg(seq_lens, i32, (R,), "seq_lens"),
+        _arg(q, bf, (T, H, D), "q", dev), _arg(k, bf, (T, H_kv, D), "k", dev), _arg(v, bf, (T, H_kv, D), "v", dev),
+        _arg(log_decay, f32, (T, H) if by_token else (H,), "log_decay", dev), int(by_token), st,
+        st if state_out is None else _arg(state_out, f32, (num_states, H, D, D), "state_out", dev),
+        _arg(state_indices, i32, (R,), "state_indices", dev), _arg(out, bf, (T, H, D), "out", dev),
+        _arg(query_start_loc, i32, (R + 1,), "query_start_loc", dev), _arg(seq_lens, i32, (R,), "seq_lens", dev),
         R, T, int(max_q_len), num_states, H, H_kv, D, float(scale),
-        _arg(workspace, torch.uint8, (ws_bytes,), "workspace"), ws_bytes,
-        _arg(err_word, i32, (1,), "err_word"), _stream(stream)))
+        _arg(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes,
+        _arg(err_word, i32, (1,), "err_word", dev), strm))

@@ -5,8 +5,9 @@
 
 namespace yoco {
 
-// What the cache of the tensor-core path holds.
-constexpr int kBf16 = 0, kE4m3 = 1, kE2m1 = 2;
+// What the cache of the tensor-core path holds (kE2m1Few: e2m1, read for at
+// most 4 heads of a kv head).
+constexpr int kBf16 = 0, kE4m3 = 1, kE2m1 = 2, kE2m1Few = 3;
 
 // Launch parameters common to both attention paths.
 struct AttnParams {

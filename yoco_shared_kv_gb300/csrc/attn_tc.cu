@@ -46,6 +46,10 @@ size_t tc_workspace_bytes(int sms, int H_kv, int G, int D, int BS, int format) {
                                           : nw_of<kBf16, 1>(D, BS);
         const size_t b1 = need(nw1, 8);
         if (b1 > b) b = b1;
+        if (format == kE2m1) {  // the walk for at most 4 heads
+            const size_t b4 = need(nw_of<kE2m1Few, 1>(D, BS), 4);
+            if (b4 > b) b = b4;
+        }
     }
     return b;
 }

@@ -75,19 +75,25 @@ namespace {
 #define YOCO_TC_F8_RING 196608
 #endif
 // e2m1 cache: warps per CTA (head_dim 128 with one and with two 8-head tiles,
-// head_dim 256 with one tile and as warp pairs), and shared-memory bytes of
+// head_dim 256 with one tile and as warp pairs, both with few heads), and shared-memory bytes of
 // the warps' stages
 #ifndef YOCO_TC_F4_NW128
-#define YOCO_TC_F4_NW128 16
+#define YOCO_TC_F4_NW128 12
 #endif
 #ifndef YOCO_TC_F4_NW128W
 #define YOCO_TC_F4_NW128W 8
 #endif
 #ifndef YOCO_TC_F4_NW256
-#define YOCO_TC_F4_NW256 12
+#define YOCO_TC_F4_NW256 8
 #endif
 #ifndef YOCO_TC_F4_NW256P
 #define YOCO_TC_F4_NW256P 8
+#endif
+#ifndef YOCO_TC_F4_NW256F
+#define YOCO_TC_F4_NW256F 12
+#endif
+#ifndef YOCO_TC_F4_NW128F
+#define YOCO_TC_F4_NW128F 16
 #endif
 #ifndef YOCO_TC_F4_RING
 #define YOCO_TC_F4_RING 196608
@@ -96,13 +102,16 @@ namespace {
 
 // FMT: what the cache holds: bf16, e4m3 (F8: one byte per element) or e2m1
 // (F4: two elements per byte, one scale byte per 32 head dims of a token).
+// FEW: e2m1 and at most 4 heads: the head tile's columns 4-7 repeat 0-3, and
+// take the odd head dims of the output where columns 0-3 take the even ones,
+// so that a byte of V (two head dims of a token) is an operand as it stands.
 // NT: 8-head tiles of a warp (1 for groups up to 8, else 2).
 // PR: warp pairs (NT = 1): the two warps of a pair walk the same pages from
 // one ring, each taking one of the group's two 8-head tiles, so a 16-column
 // walk runs on twice the warps in the same shared memory.
 template <int D, int BS, int FMT = kBf16, int NT = 2, bool PR = false>
 struct TcShape {
-    static constexpr bool F8 = FMT == kE4m3, F4 = FMT == kE2m1;
+    static constexpr bool F8 = FMT == kE4m3, F4 = FMT == kE2m1 || FMT == kE2m1Few, FEW = FMT == kE2m1Few;
     static_assert(!PR || NT == 1, "a warp of a pair takes one 8-head tile");
     static constexpr int ESZ = F8 ? 1 : 2;                // bytes per cached element (not e2m1)
     static constexpr int ROW_BYTES = F4 ? D / 2 : D * ESZ;  // K (or V) of one token, one kv head
@@ -110,7 +119,7 @@ struct TcShape {
     static constexpr int STAGE_BYTES = 2 * PAGE_BYTES;    // K + V
     static constexpr int NTG = PR ? 2 : NT;               // 8-head tiles of the group
     // a worker's (warp's, or pair's) two end-of-slice pieces at the largest group
-    static constexpr int PIECE_PAIR = 2 * (8 * NTG * (D * 4 + 8) + 16);
+    static constexpr int PIECE_PAIR = 2 * ((FEW ? 4 : 8 * NTG) * (D * 4 + 8) + 16);
     // the most workers (8, 4, 2) whose ring share holds two stages and the two pieces
     static constexpr int F8_FITS8 =
         PIECE_PAIR <= YOCO_TC_F8_RING / 8 && 2 * STAGE_BYTES <= YOCO_TC_F8_RING / 8;
@@ -124,8 +133,14 @@ struct TcShape {
     static constexpr bool QSM = D == 256 && NT == 2 && !F4;
     // e2m1: as many warps as the registers of their accumulators allow (the walk is
     // bound by instructions, not by the bytes in flight)
-    static constexpr int F4_NW = D == 256 ? (NTG == 2 ? YOCO_TC_F4_NW256P / 2 : YOCO_TC_F4_NW256)
-                                          : (NTG == 2 ? YOCO_TC_F4_NW128W / (PR ? 2 : 1) : YOCO_TC_F4_NW128);
+    static constexpr int F4_NW =
+        FEW        ? (D == 256 ? (BS == 32 && YOCO_TC_F4_NW256F > 12 ? 12 : YOCO_TC_F4_NW256F) : YOCO_TC_F4_NW128F)
+        : D == 256 ? (NTG == 2 ? YOCO_TC_F4_NW256P / 2 : YOCO_TC_F4_NW256)
+                   : (NTG == 2 ? YOCO_TC_F4_NW128W / (PR ? 2 : 1) : YOCO_TC_F4_NW128);
+    // pages a step takes: two of 16 tokens, but for one warp's walk at head_dim 256
+    // (measured on 64 requests of 1024..8192 keys: 49 us a layer with one, 53 with two;
+    // head_dim 128 36 and 35, warp pairs 122 and 114)
+    static constexpr int F4_PG = BS == 16 && (D == 128 || PR) ? 2 : 1;
     static constexpr int F4_SREC = 2 * BS * (D / 32);  // scale bytes of a (page, kv head): K, then V
     // workers (each with its own ring and slice), and warps
     static constexpr int WK =
@@ -139,7 +154,7 @@ struct TcShape {
     static constexpr int F4_RING = (YOCO_TC_F4_RING / WK) & ~1023;
     static constexpr int F4_STAGES = F4_RING / STAGE_BYTES;
     static constexpr int STAGES =
-        F4 ? (F4_STAGES > 6 ? 6 : F4_STAGES)
+        F4 ? (F4_STAGES > 6 ? 6 : F4_STAGES < 2 ? 2 : F4_STAGES)
         : F8 ? (F8_STAGES < 2 ? 2 : F8_STAGES)
            : (STAGE_BYTES == 16384 ? ((QSM || PR) ? 3 : YOCO_TC_ST16) : 3);
     // elements (bytes for e2m1) per row of a swizzled sub-tile: 128 bytes, or
@@ -159,9 +174,12 @@ struct TcShape {
     static constexpr int WBUF =
         F4 && PIECE_PAIR > STAGES * STAGE_BYTES ? (PIECE_PAIR + 1023) & ~1023 : STAGES * STAGE_BYTES;
     static constexpr int RING_BYTES = WK * WBUF;
-    // e2m1: every stage's scale record, and per warp the V multipliers of the
-    // page in hand (f16 [D / 32][BS])
-    static constexpr int F4_MUL = (D / 32) * BS * 2;
+    // e2m1: every stage's scale record, and per warp the multipliers of the 16
+    // tokens in hand: a word of K and one of V (half a word without FEW) for
+    // each 32 head dims, rows of 20 words so that a warp's writes spread over
+    // the banks
+    static constexpr int F4_ROW = 20;
+    static constexpr int F4_MUL = 2 * (D / 32) * F4_ROW * 4;
     static constexpr int F4_BYTES = F4 ? WK * STAGES * F4_SREC + NW * F4_MUL : 0;
     static constexpr int SMEM = RING_BYTES + NW * Q_BYTES + F4_BYTES + 1024;
     static_assert(SMEM <= 225 * 1024, "the rings must leave room for static shared memory");
@@ -795,7 +813,8 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     attn_tc_persistent(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
     using S = TcShape<D, BS, FMT, NT, PR>;
-    constexpr bool F8 = S::F8, F4 = S::F4;
+    constexpr bool F8 = S::F8, F4 = S::F4, FEW = S::FEW;
+    constexpr int OT = FEW ? D / 32 : S::KD;  // 16-row steps of the output accumulators
     constexpr int NW = S::NW, WK = S::WK, STAGES = S::STAGES, NTG = S::NTG;
     static_assert(S::PIECE_PAIR <= S::WBUF,
                   "a worker's two end-of-slice pieces must fit in its ring");
@@ -829,7 +848,9 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     uint8_t* wbuf = smem + wk * S::WBUF;
     // e2m1: the worker's scale records, stage by stage, and this warp's V multipliers
     uint8_t* const srec4 = smem + S::RING_BYTES + wk * STAGES * S::F4_SREC;
-    uint8_t* const vmul4 = smem + S::RING_BYTES + WK * STAGES * S::F4_SREC + warp * S::F4_MUL;
+    uint32_t* const kmul4 = reinterpret_cast<uint32_t*>(smem + S::RING_BYTES + WK * STAGES * S::F4_SREC +
+                                                        warp * S::F4_MUL);
+    uint32_t* const vmul4 = kmul4 + (D / 32) * S::F4_ROW;
     uint64_t* wbar = bars + wk * STAGES;
     if (lane == 0 && leader) {  // each worker's ring barriers: only its warps wait on them
         for (int i = 0; i < STAGES; ++i) mbar_init(&wbar[i], 1);
@@ -922,6 +943,10 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     // lane 0: block-table entry of page pc, loaded one issue ahead so that its
     // latency overlaps the page computed in between
     int32_t blk_next = -1;
+    // (e2m1 issues two pages at a time: the entry behind it as well, where it is the
+    // same segment's)
+    constexpr int32_t kUnread = INT32_MIN;
+    int32_t blk_after = kUnread;
     auto fetch_blk = [&]() {
         blk_next = __ldg(p.block_table + static_cast<int64_t>(pc.req) * p.max_blocks + pc.pp);
     };
@@ -1067,17 +1092,20 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
         }
     }
     uint32_t qf[S::QSM ? 1 : S::KD][NT][2];  // queries in registers (not with QSM)
-    float o[S::KD][NT][4];
+    float o[OT][NT][4];
     float m_run[NT][2], l_part[NT][2];
     // e4m3: o holds sum p * (v_scale / vref) * code; vref is the V scale of the
     // segment's first page here, moved (and o rescaled) when a page's ratio
     // leaves [1/16, 16], so that the f16 weights stay in range
     float vref = 0.f, vinv = 0.f;
-    // e2m1: score factor of each column (with its query's power of two); the
-    // scale byte that the weights are taken against: o holds
-    // sum 2^8 p * 2^(b - vtop + 7) * code, vtop the largest V scale byte walked
-    // so far (never under 30), so that p down to 2^-22 and scales down to
-    // 2^-21 of the largest are whole f16 numbers. vref turns o into true units.
+    // e2m1: score factor of each column (with its query's power of two). The
+    // weights are f16 numbers 2^(score - m + 3), m a reference that follows the
+    // running maximum in steps of more than 5 (in log2 units), so that almost no
+    // page rescales o; they take V's scale against vtop, the largest V scale byte
+    // walked so far (never under 30), as 2^(b - vtop + 7): at most 2^15 together,
+    // whole f16 numbers for weights down to 2^-17 and scales down to 2^-21 of the
+    // largest. o holds their sums; vref turns it into true units.
+    constexpr float kLazy = 5.f, kBias = 3.f;
     float qscale[NT][2];
     int32_t vtop = 30;
     auto reset_state = [&]() {
@@ -1087,7 +1115,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
             vref = __uint_as_float(static_cast<uint32_t>(30 - 7) << 23);
         }
 #pragma unroll
-        for (int a = 0; a < S::KD; ++a)
+        for (int a = 0; a < OT; ++a)
 #pragma unroll
             for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -1176,7 +1204,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int h = c8 + nt * 8 + gl;
+                const int h = FEW ? gl & 3 : c8 + nt * 8 + gl;
                 bool ok;
                 int hr = 0, hh = 0;
                 if constexpr (RG) {
@@ -1267,7 +1295,8 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     };
     // head dim of accumulator row gl (half 0) / gl + 8 (half 1) of 16-wide step md
     auto drow = [&](int md, int half) {
-        return F4   ? (md >> 1) * 32 + 4 * gl + 2 * (md & 1) + half
+        return FEW  ? md * 32 + 4 * gl + 2 * half + (tq >> 1)
+               : F4 ? (md >> 1) * 32 + 4 * gl + 2 * (md & 1) + half
                : F8 ? md * 16 + 2 * gl + half
                     : md * 16 + gl + 8 * half;
     };
@@ -1290,7 +1319,268 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
             break;
         }
         consumed = i + 1;
-        if (stage_blk[wk * STAGES + st] >= 0) {
+        bool two = false;  // this step takes the next page of the walk as well (e2m1)
+        if constexpr (F4) {
+            // One page a step, or (PG = 2) the next one too when it belongs to this segment
+            // and slice, so that the work of a step that does not grow with its tokens is
+            // done once for both.
+            constexpr int PG = S::F4_PG, MT = S::MT, TT = PG * MT, GD = D / 32;
+            const int st2 = PG == 2 ? (i + 1) % STAGES : st;
+            if constexpr (PG == 2) {
+                two = i + 1 < n_my && cc.pp != (rev ? 0 : cc.pages - 1);
+                if (two) {
+                    landed = mbar_wait_bounded(wbar + st2, ((i + 1) / STAGES) & 1, kWaitLimitNs);
+                    if constexpr (PR) landed = pair_all(pair_bar, landed);
+                    if (!landed) {
+                        aborted = true;
+                        break;
+                    }
+                    consumed = i + 2;
+                }
+            }
+            // Of each tile: its stage, its keys in reach of the group's last row (none in a
+            // page that is not there), its tokens' first key and scale bytes (K, then V)
+            int32_t keys[TT];
+            uint32_t kb[TT];
+            const uint8_t* sr[TT];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                const int pg = tt / MT, mt = tt % MT, ps = pg ? st2 : st;
+                const int32_t pp = cc.pp + (rev ? -pg : pg);
+                const bool there = (pg == 0 || two) && stage_blk[wk * STAGES + ps] >= 0;
+                keys[tt] = there ? cc.kv_len - pp * BS - mt * 16 : 0;
+                kb[tt] = smem_u32(wbuf + ps * S::STAGE_BYTES) + mt * 16 * S::ROW_BYTES;
+                sr[tt] = srec4 + ps * S::F4_SREC + mt * 16 * GD;
+            }
+            {
+                // the largest V scale of the tokens in reach (later bytes may be stale)
+                int32_t top = 0;
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {  // a lane's bytes belong to one token
+                    const uint8_t* sv = sr[tt] + BS * GD;
+                    if constexpr (GD == 8) {
+                        if (lane >> 1 < keys[tt])
+                            top = max(top, max_byte(reinterpret_cast<const uint32_t*>(sv)[lane]));
+                    } else {
+                        if (lane >> 1 < keys[tt])
+                            top = max(top, max_byte(reinterpret_cast<const uint16_t*>(sv)[lane]));
+                    }
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+                if (top > vtop) {  // warp-uniform, rare
+                    const float f = top - vtop < 127
+                                        ? __uint_as_float(static_cast<uint32_t>(127 + vtop - top) << 23)
+                                        : 0.f;
+#pragma unroll
+                    for (int md = 0; md < OT; ++md)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[md][nt][c] *= f;
+                    vtop = top;
+                    vref = __uint_as_float(static_cast<uint32_t>(top - 7) << 23);
+                }
+            }
+            // multipliers of a tile's 16 tokens, from its scale bytes to this warp's words
+            // (a lane has 4 bytes, one token's: at head_dim 128 the upper lanes have none)
+            auto tile_scales = [&](int tt, bool of_k) {
+                const int t = lane * 4 / GD, g0 = lane * 4 % GD;
+                if (GD == 8 || lane < 16) {
+                    const uint32_t w =
+                        *reinterpret_cast<const uint32_t*>(sr[tt] + (of_k ? 0 : BS * GD) + t * GD + g0);
+                    if (of_k) {  // fp32, tokens t and t + 8 next to each other
+                        uint32_t* dst = kmul4 + g0 * S::F4_ROW + 2 * (t & 7) + (t >> 3);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dst[j * S::F4_ROW] = __float_as_uint(scale_of_byte(w, j));
+                    } else {  // f16 (FEW: twice), tokens 2j, 2j + 1, 2j + 8, 2j + 9 next to each other
+                        const int at = 4 * ((t & 7) >> 1) + (t & 1) + 2 * (t >> 3);
+                        const bool in_reach = t < keys[tt];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int32_t e = static_cast<int32_t>((w >> (8 * j)) & 255u) - vtop + 22;
+                            const uint32_t m = in_reach && e > 0 ? static_cast<uint32_t>(e) << 10 : 0u;
+                            if constexpr (FEW)
+                                vmul4[(g0 + j) * S::F4_ROW + at] = m * 0x10001u;
+                            else
+                                reinterpret_cast<uint16_t*>(vmul4)[(g0 + j) * S::F4_ROW + at] =
+                                    static_cast<uint16_t>(m);
+                        }
+                    }
+                }
+            };
+            const int mi = lane >> 3, rr = lane & 7;
+            const uint32_t lane_at = swz4<S::ROW_BYTES>((mi & 1) * 8 + rr, mi >> 1);  // of an ldmatrix
+            // ---- S^T = K Q^T (tokens x heads) ----
+            // One ldmatrix.x4 = 16 tokens x 64 head dims; a lane's 32-bit register holds 8
+            // consecutive codes of one token, which widen to f16 exactly. Each 32 dims'
+            // products (two k steps from zero) enter the score with their token's scale, so
+            // that no code is multiplied by it.
+            float sc[TT][NT][4];
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                if (tt / MT == 1 && !two) {  // warp-uniform
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) sc[tt][nt][c] = -INFINITY;
+                    continue;
+                }
+                __syncwarp();  // the last tile's words have been read
+                tile_scales(tt, true);
+                if constexpr (TT == 1) tile_scales(tt, false);
+                __syncwarp();
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sc[tt][nt][c] = 0.f;
+#pragma unroll
+                for (int kp = 0; kp < GD / 2; ++kp) {
+                    uint32_t r[4];
+                    ldsm_x4(kb[tt] + (lane_at ^ (kp << 5)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * kp + h;  // these 32 head dims
+                        uint32_t a[4], b[4];
+                        e2m1x8_to_f16x2(r[2 * h], a[0], a[1], a[2], a[3]);
+                        e2m1x8_to_f16x2(r[2 * h + 1], b[0], b[1], b[2], b[3]);
+                        const float2 ks = *reinterpret_cast<const float2*>(kmul4 + g * S::F4_ROW + 2 * gl);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float d[4];
+                            mma_f16_16816_zero(d, a[0], b[0], a[1], b[1], qf[2 * g][nt][0], qf[2 * g][nt][1]);
+                            mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * g + 1][nt][0], qf[2 * g + 1][nt][1]);
+                            sc[tt][nt][0] = fmaf(d[0], ks.x, sc[tt][nt][0]);
+                            sc[tt][nt][1] = fmaf(d[1], ks.x, sc[tt][nt][1]);
+                            sc[tt][nt][2] = fmaf(d[2], ks.y, sc[tt][nt][2]);
+                            sc[tt][nt][3] = fmaf(d[3], ks.y, sc[tt][nt][3]);
+                        }
+                    }
+                }
+                // keys past a row's causal end (moff: the rows of a group end one key apart)
+                if (keys[tt] - (RG ? cc.nr - 1 : 0) < 16) {  // warp-uniform
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int lim0 = keys[tt] - (RG ? moff[nt][0] : 0);
+                        const int lim1 = keys[tt] - (RG ? moff[nt][1] : 0);
+                        float* c = sc[tt][nt];
+                        if (gl >= lim0) c[0] = -INFINITY;
+                        if (gl >= lim1) c[1] = -INFINITY;
+                        if (gl + 8 >= lim0) c[2] = -INFINITY;
+                        if (gl + 8 >= lim1) c[3] = -INFINITY;
+                    }
+                }
+            }
+            // ---- online softmax over the step's tokens ----
+            // A column without a key yet keeps m = -inf; its weights are taken against 0,
+            // so that they are 0 and never NaN.
+            uint32_t pb[TT][NT][2];  // weights in f16; the row sums take them unrounded
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float mx0 = fmaxf(sc[0][nt][0], sc[0][nt][2]), mx1 = fmaxf(sc[0][nt][1], sc[0][nt][3]);
+#pragma unroll
+                for (int tt = 1; tt < TT; ++tt) {
+                    mx0 = fmaxf(mx0, fmaxf(sc[tt][nt][0], sc[tt][nt][2]));
+                    mx1 = fmaxf(mx1, fmaxf(sc[tt][nt][1], sc[tt][nt][3]));
+                }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+                }
+                mx0 *= qscale[nt][0];
+                mx1 *= qscale[nt][1];
+                // the reference moves by more than kLazy or not at all
+                const bool up0 = mx0 > m_run[nt][0] + kLazy, up1 = mx1 > m_run[nt][1] + kLazy;
+                if (__any_sync(0xffffffffu, up0 || up1)) {
+                    const float c0 = up0 ? exp2_approx(m_run[nt][0] - mx0) : 1.f;
+                    const float c1 = up1 ? exp2_approx(m_run[nt][1] - mx1) : 1.f;
+                    if (up0) m_run[nt][0] = mx0;
+                    if (up1) m_run[nt][1] = mx1;
+#pragma unroll
+                    for (int md = 0; md < OT; ++md) {
+                        o[md][nt][0] *= c0;
+                        o[md][nt][1] *= c1;
+                        o[md][nt][2] *= c0;
+                        o[md][nt][3] *= c1;
+                    }
+                    l_part[nt][0] *= c0;
+                    l_part[nt][1] *= c1;
+                }
+                const float n0 = kBias - (m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0]);
+                const float n1 = kBias - (m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1]);
+#pragma unroll
+                for (int tt = 0; tt < TT; ++tt) {
+                    const float* c = sc[tt][nt];
+                    const float p0 = exp2_approx(fmaf(c[0], qscale[nt][0], n0));
+                    const float p1 = exp2_approx(fmaf(c[1], qscale[nt][1], n1));
+                    const float p2 = exp2_approx(fmaf(c[2], qscale[nt][0], n0));
+                    const float p3 = exp2_approx(fmaf(c[3], qscale[nt][1], n1));
+                    l_part[nt][0] += p0 + p2;
+                    l_part[nt][1] += p1 + p3;
+                    pb[tt][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                    pb[tt][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
+                }
+            }
+            // ---- O^T += V^T P^T ----
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) {
+                if (tt / MT == 1 && !two) continue;
+                if constexpr (TT > 1) {
+                    __syncwarp();  // the last tile's words have been read
+                    tile_scales(tt, false);
+                    __syncwarp();
+                }
+                const uint32_t vb = kb[tt] + S::PAGE_BYTES;
+                // FEW: the weight of token 2tq (2tq + 1) of the lower and upper 8 tokens in the
+                // half of its column's head dim, even or odd
+                uint32_t w[4];
+                if constexpr (FEW) {
+                    const uint32_t s0 = gl < 4 ? 0x4410u : 0x1044u, s1 = gl < 4 ? 0x4432u : 0x3244u;
+                    w[0] = __byte_perm(pb[tt][0][0], 0u, s0);
+                    w[1] = __byte_perm(pb[tt][0][0], 0u, s1);
+                    w[2] = __byte_perm(pb[tt][0][1], 0u, s0);
+                    w[3] = __byte_perm(pb[tt][0][1], 0u, s1);
+                }
+#pragma unroll
+                for (int mp = 0; mp < GD / 2; ++mp) {
+                    uint32_t r[4];
+                    ldsm_x4_trans(vb + (lane_at ^ (mp << 5)), r[0], r[1], r[2], r[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int g = 2 * mp + h;
+                        if constexpr (FEW) {
+                            // ldmatrix.trans over 16-bit units hands a lane bytes 2gl and 2gl + 1
+                            // (head dims 4gl..4gl+3) of tokens 2tq and 2tq + 1: rows gl and gl + 8
+                            // of k slots tq and tq + 4, a slot being the two head dims of a byte
+                            const uint4 m = *reinterpret_cast<const uint4*>(vmul4 + g * S::F4_ROW + 4 * tq);
+                            uint32_t x[4], y[4];
+                            e2m1x8_to_f16x2(r[2 * h], x[0], x[1], x[2], x[3]);
+                            e2m1x8_to_f16x2(r[2 * h + 1], y[0], y[1], y[2], y[3]);
+                            mma_f16_16816(o[g][0], x[0], x[1], x[2], x[3], mul_f16x2(w[0], m.x),
+                                          mul_f16x2(w[1], m.y));
+                            mma_f16_16816(o[g][0], y[0], y[1], y[2], y[3], mul_f16x2(w[2], m.z),
+                                          mul_f16x2(w[3], m.w));
+                        } else {
+                            // the same units, codes of the two tokens paired: A-operand row gl
+                            // takes dim 4gl (4gl + 2) and row gl + 8 dim 4gl + 1 (4gl + 3) of the
+                            // 32 dims' first (second) 16-row step
+                            const uint2 m = *reinterpret_cast<const uint2*>(
+                                reinterpret_cast<const uint16_t*>(vmul4) + g * S::F4_ROW + 4 * tq);
+                            uint32_t x[4], y[4];  // dims 4gl + j of the lower / upper 8 tokens
+                            e2m1_pairs_to_f16x2(r[2 * h], x);
+                            e2m1_pairs_to_f16x2(r[2 * h + 1], y);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const uint32_t b0 = mul_f16x2(pb[tt][nt][0], m.x);
+                                const uint32_t b1 = mul_f16x2(pb[tt][nt][1], m.y);
+                                mma_f16_16816(o[2 * g][nt], x[0], x[1], y[0], y[1], b0, b1);
+                                mma_f16_16816(o[2 * g + 1][nt], x[2], x[3], y[2], y[3], b0, b1);
+                            }
+                        }
+                    }
+                }
+            }
+        } else if (stage_blk[wk * STAGES + st] >= 0) {
             const uint32_t kbase = smem_u32(wbuf + st * S::STAGE_BYTES);
             const uint32_t vbase = kbase + S::PAGE_BYTES;
             const int32_t nvalid = min(BS, cc.kv_len - cc.pp * BS);
@@ -1320,42 +1610,6 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                     vr = 1.f;
                 }
             }
-            if constexpr (F4) {
-                // The page's V multipliers 2^(b - vtop + 7) as f16 (none for tokens past
-                // the causal end, whose bytes may be stale), laid out [32 dims][token] so
-                // that a lane's token pair is one word.
-                constexpr int GD = D / 32, NV = BS * GD / 32;  // scale bytes a lane takes
-                const uint8_t* sv = srec4 + st * S::F4_SREC + BS * GD;
-                int32_t b[NV], top = 0;
-#pragma unroll
-                for (int u = 0; u < NV; ++u) {  // byte u * 32 + lane = token * GD + group
-                    const int x = u * 32 + lane;
-                    b[u] = x / GD < nvalid ? sv[x] : 0;
-                    top = max(top, b[u]);
-                }
-                top = __reduce_max_sync(0xffffffffu, top);
-                if (top > vtop) {  // warp-uniform, rare
-                    const float f = top - vtop < 127
-                                        ? __uint_as_float(static_cast<uint32_t>(127 + vtop - top) << 23)
-                                        : 0.f;
-#pragma unroll
-                    for (int md = 0; md < S::KD; ++md)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[md][nt][c] *= f;
-                    vtop = top;
-                    vref = __uint_as_float(static_cast<uint32_t>(top - 7) << 23);
-                }
-                __syncwarp();  // the previous page's multipliers have been read
-#pragma unroll
-                for (int u = 0; u < NV; ++u) {
-                    const int x = u * 32 + lane;
-                    reinterpret_cast<uint16_t*>(vmul4)[(x % GD) * BS + x / GD] =
-                        static_cast<uint16_t>(max(b[u] - vtop + 22, 0) << 10);
-                }
-                __syncwarp();
-            }
             if (fused && cc.pp == (cc.kv_len - 1) / BS) {
                 // Fused decode step: the row's newest key is this step's token, which
                 // this launch also appends to the pools; whatever the page copy
@@ -1382,7 +1636,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                 fence_proxy_async_smem();  // before a later copy refills the stage
                 __syncwarp();
             }
-            if (!F4 && nvalid < BS) {
+            if (nvalid < BS) {
                 // Rows past the causal end may hold stale data (even NaN), and a
                 // zero probability times NaN is NaN: clear those V rows first.
                 // (a pair's warps clear alternate sub-tiles, then meet)
@@ -1398,55 +1652,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
             }
             // ---- S^T = K Q^T (tokens x heads); two accumulators halve the chain ----
             float sc[S::MT][NT][4];
-            if constexpr (F4) {
-                // One ldmatrix.x4 = 16 tokens x 64 head dims; a lane's 32-bit register holds
-                // 8 consecutive codes of one token, which widen to f16 exactly. Each 32
-                // dims' products (two k steps from zero) enter the score with their
-                // token's scale, so that no code is multiplied by it.
-                constexpr int GD = D / 32;
-                const int mi = lane >> 3, rr = lane & 7;
-                const uint8_t* sk = srec4 + st * S::F4_SREC;
-#pragma unroll
-                for (int mt = 0; mt < S::MT; ++mt) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) sc[mt][nt][c] = 0.f;
-                    uint32_t w0[GD / 4], w1[GD / 4];  // scale bytes of tokens gl and gl + 8
-#pragma unroll
-                    for (int i = 0; i < GD / 4; ++i) {
-                        w0[i] = *reinterpret_cast<const uint32_t*>(sk + (mt * 16 + gl) * GD + 4 * i);
-                        w1[i] = *reinterpret_cast<const uint32_t*>(sk + (mt * 16 + gl + 8) * GD + 4 * i);
-                    }
-                    const int t = mt * 16 + (mi & 1) * 8 + rr;
-#pragma unroll
-                    for (int kp = 0; kp < GD / 2; ++kp) {
-                        uint32_t r[4];
-                        ldsm_x4(kbase + swz4<S::ROW_BYTES>(t, 2 * kp + (mi >> 1)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = 2 * kp + h;  // these 32 head dims
-                            uint32_t a[4], b[4];
-                            e2m1x8_to_f16x2(r[2 * h], a[0], a[1], a[2], a[3]);
-                            e2m1x8_to_f16x2(r[2 * h + 1], b[0], b[1], b[2], b[3]);
-                            const float s0 = scale_of_byte(w0[g >> 2], g & 3);
-                            const float s1 = scale_of_byte(w1[g >> 2], g & 3);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                float d[4];
-                                mma_f16_16816_zero(d, a[0], b[0], a[1], b[1], qf[2 * g][nt][0],
-                                                   qf[2 * g][nt][1]);
-                                mma_f16_16816(d, a[2], b[2], a[3], b[3], qf[2 * g + 1][nt][0],
-                                              qf[2 * g + 1][nt][1]);
-                                sc[mt][nt][0] = fmaf(d[0], s0, sc[mt][nt][0]);
-                                sc[mt][nt][1] = fmaf(d[1], s0, sc[mt][nt][1]);
-                                sc[mt][nt][2] = fmaf(d[2], s1, sc[mt][nt][2]);
-                                sc[mt][nt][3] = fmaf(d[3], s1, sc[mt][nt][3]);
-                            }
-                        }
-                    }
-                }
-            } else {
+            {
                 float sc2[S::MT][NT][4];
 #pragma unroll
                 for (int mt = 0; mt < S::MT; ++mt)
@@ -1610,8 +1816,8 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
                 }
-                const float mn0 = fmaxf(m_run[nt][0], mx0 * (F4 ? qscale[nt][0] : sl2p));
-                const float mn1 = fmaxf(m_run[nt][1], mx1 * (F4 ? qscale[nt][1] : sl2p));
+                const float mn0 = fmaxf(m_run[nt][0], mx0 * sl2p);
+                const float mn1 = fmaxf(m_run[nt][1], mx1 * sl2p);
                 // a column with no key yet (a group row whose keys all lie on later
                 // pages of a backward walk) keeps m = -inf: its weights and factor
                 // are taken against 0, so that they are 0 and never NaN
@@ -1637,56 +1843,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                 l_part[nt][1] *= corr[nt][1];
             }
             // ---- O^T += V^T P^T ----
-            if constexpr (F4) {
-                uint32_t pb[S::MT][NT][2];  // 2^8 p in f16; the row sums take them unrounded
-#pragma unroll
-                for (int kt = 0; kt < S::MT; ++kt)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float* c = sc[kt][nt];
-                        const float p0 = exp2_approx(fmaf(c[0], qscale[nt][0], 8.f - msafe[nt][0]));
-                        const float p1 = exp2_approx(fmaf(c[1], qscale[nt][1], 8.f - msafe[nt][1]));
-                        const float p2 = exp2_approx(fmaf(c[2], qscale[nt][0], 8.f - msafe[nt][0]));
-                        const float p3 = exp2_approx(fmaf(c[3], qscale[nt][1], 8.f - msafe[nt][1]));
-                        l_part[nt][0] += p0 + p2;
-                        l_part[nt][1] += p1 + p3;
-                        pb[kt][nt][0] = movmatrix_trans(pack_f16x2(p0, p1));
-                        pb[kt][nt][1] = movmatrix_trans(pack_f16x2(p2, p3));
-                    }
-                // ldmatrix.trans over 16-bit units hands a lane head dims 4gl..4gl+3 of
-                // tokens 2tq (low half) and 2tq + 1 of each 32 dims: A-operand row gl
-                // takes dim 4gl (4gl + 2) and row gl + 8 dim 4gl + 1 (4gl + 3) of the 32
-                // dims' first (second) 16-row step. The weights, not the codes, take the
-                // token's scale: two products serve both steps.
-                constexpr int GD = D / 32;
-                const int mi = lane >> 3, rr = lane & 7;
-                const uint32_t* mul = reinterpret_cast<const uint32_t*>(vmul4) + tq;
-#pragma unroll
-                for (int mp = 0; mp < GD / 2; ++mp) {
-#pragma unroll
-                    for (int kt = 0; kt < S::MT; ++kt) {
-                        const int t = kt * 16 + (mi & 1) * 8 + rr;
-                        uint32_t r[4];
-                        ldsm_x4_trans(vbase + swz4<S::ROW_BYTES>(t, 2 * mp + (mi >> 1)), r[0], r[1], r[2], r[3]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = 2 * mp + h;
-                            const uint32_t mlo = mul[g * (BS / 2) + kt * 8];
-                            const uint32_t mhi = mul[g * (BS / 2) + kt * 8 + 4];
-                            uint32_t x[4], y[4];  // dims 4gl + i of the lower / upper 8 tokens
-                            e2m1_pairs_to_f16x2(r[2 * h], x);
-                            e2m1_pairs_to_f16x2(r[2 * h + 1], y);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint32_t b0 = mul_f16x2(pb[kt][nt][0], mlo);
-                                const uint32_t b1 = mul_f16x2(pb[kt][nt][1], mhi);
-                                mma_f16_16816(o[2 * g][nt], x[0], x[1], y[0], y[1], b0, b1);
-                                mma_f16_16816(o[2 * g + 1][nt], x[2], x[3], y[2], y[3], b0, b1);
-                            }
-                        }
-                    }
-                }
-            } else if constexpr (F8) {
+            if constexpr (F8) {
                 // weights p * vr in f16 for all 16-token tiles; the row sums take p
                 uint32_t pb[S::MT][NT][2];
 #pragma unroll
@@ -1771,7 +1928,27 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
         // the stage is free once every warp reading it is done (both of a pair)
         if constexpr (PR) pair_sync(pair_bar);
         else __syncwarp();
-        if (lane == 0 && leader && i + STAGES < n_my) {
+        if constexpr (F4) {
+            if (lane == 0 && leader && i + STAGES < n_my) {
+                issue(i + STAGES);
+                if (two && i + 1 + STAGES < n_my) {
+                    if (blk_after != kUnread) blk_next = blk_after;
+                    else fetch_blk();
+                    issue(i + 1 + STAGES);
+                }
+                if (i + (two ? 2 : 1) + STAGES < n_my) {
+                    fetch_blk();
+                    const int32_t pp = pc.pp + (rev ? -1 : 1);
+                    blk_after = pp >= 0 && pp < pc.pages
+                                    ? __ldg(p.block_table + static_cast<int64_t>(pc.req) * p.max_blocks + pp)
+                                    : kUnread;
+                }
+            }
+            if (two) {  // on to the second page
+                ++i;
+                cc.pp += rev ? -1 : 1;
+            }
+        } else if (lane == 0 && leader && i + STAGES < n_my) {
             issue(i + STAGES);
             if (i + STAGES + 1 < n_my) fetch_blk();
         }
@@ -1793,7 +1970,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int h = c8 + nt * 8 + 2 * tq + e;
+                        const int h = FEW ? (2 * tq + e) & 3 : c8 + nt * 8 + 2 * tq + e;
                         // a group row without any key (seq_len below its request's rows)
                         // is zero-filled and flagged above: never written here
                         if (h >= nvh || (RG && l_part[nt][e] == 0.f)) continue;
@@ -1802,7 +1979,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                         __nv_bfloat16* dst =
                             outp + ((static_cast<int64_t>(cc.n) + hr) * p.H_q + cc.g * p.G + (h - hr * p.G)) * D;
 #pragma unroll
-                        for (int md = 0; md < S::KD; ++md) {
+                        for (int md = 0; md < OT; ++md) {
                             dst[drow(md, 0)] = __float2bfloat16_rn(o[md][nt][e] * inv);
                             dst[drow(md, 1)] = __float2bfloat16_rn(o[md][nt][2 + e] * inv);
                         }
@@ -1829,12 +2006,12 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int h = c8 + nt * 8 + 2 * tq + e;
+                        const int h = FEW ? (2 * tq + e) & 3 : c8 + nt * 8 + 2 * tq + e;
                         if (h >= nvh) continue;
                         float* dst = dst_o + h * D;
                         const float of = F8 || F4 ? vref : 1.f;  // partials in true units
 #pragma unroll
-                        for (int md = 0; md < S::KD; ++md) {
+                        for (int md = 0; md < OT; ++md) {
                             dst[drow(md, 0)] = o[md][nt][e] * of;
                             dst[drow(md, 1)] = o[md][nt][2 + e] * of;
                         }
@@ -2071,7 +2248,11 @@ cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const AttnP
     // as warp pairs, a one-warp two-tile kernel serves the fused step alone.
     using K = void (*)(CUtensorMap, CUtensorMap, AttnParams);
     K kernel;
-    if constexpr (FMT == kE2m1) {  // no fused step over this cache
+    if constexpr (FMT == kE2m1Few) {  // one row a segment
+        if (fuse || grouped) return cudaErrorInvalidConfiguration;
+        kernel = p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, false, PR>
+                           : attn_tc_persistent<D, BS, NT, false, FMT, false, false, PR>;
+    } else if constexpr (FMT == kE2m1) {  // no fused step over this cache
         if (fuse) return cudaErrorInvalidConfiguration;
         kernel = grouped ? (p.reverse ? attn_tc_persistent<D, BS, NT, true, FMT, false, true, PR>
                                       : attn_tc_persistent<D, BS, NT, false, FMT, false, true, PR>)
@@ -2111,6 +2292,8 @@ template <int D, int BS, int FMT>
 cudaError_t launch_bs(const CUtensorMap& mk, const CUtensorMap& mv, const AttnParams& p, int sms,
                       cudaStream_t s) {
     const bool wide = p.vhs > 8;  // two 8-head tiles: a group over 8, or 16 virtual heads
+    if constexpr (FMT == kE2m1)
+        if (p.vhs <= 4) return launch_one<D, BS, 1, kE2m1Few, false>(mk, mv, p, sms, s);
     if constexpr (tc_pairs<D, BS, FMT>()) {
         if (wide && p.k_new == nullptr) return launch_one<D, BS, 1, FMT, true>(mk, mv, p, sms, s);
     }

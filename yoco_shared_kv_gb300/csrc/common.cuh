@@ -310,13 +310,20 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t& r0, uint32
         : "r"(x));
 }
 
+// (a & m) | (b & ~m), one instruction.
+__device__ __forceinline__ uint32_t bit_select(uint32_t a, uint32_t b, uint32_t m) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+    return r;
+}
+
 // Codes 0..3 of the low 16 bits paired with codes 0..3 of the high 16 bits:
 // r[i] = f16x2 of (low code i, high code i). Even codes meet in the lower
 // bytes after a shift right by 12, odd ones in the upper bytes after a shift
-// left by 12: two logic instructions for four pairs' worth of nibbles.
+// left by 12.
 __device__ __forceinline__ void e2m1_pairs_to_f16x2(uint32_t x, uint32_t (&r)[4]) {
-    const uint32_t even = (x & 0x0f0f0f0fu) | ((x >> 12) & 0xf0f0f0f0u);  // bytes 0, 1
-    const uint32_t odd = (x & 0xf0f0f0f0u) | ((x << 12) & 0x0f0f0f0fu);   // bytes 2, 3
+    const uint32_t even = bit_select(x, x >> 12, 0x0f0f0f0fu);  // bytes 0, 1
+    const uint32_t odd = bit_select(x, x << 12, 0xf0f0f0f0u);   // bytes 2, 3
     asm("{ .reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %2;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, a; cvt.rn.f16x2.e2m1x2 %1, b; }"
         : "=r"(r[0]), "=r"(r[2])
@@ -325,6 +332,10 @@ __device__ __forceinline__ void e2m1_pairs_to_f16x2(uint32_t x, uint32_t (&r)[4]
         "cvt.rn.f16x2.e2m1x2 %0, c; cvt.rn.f16x2.e2m1x2 %1, d; }"
         : "=r"(r[1]), "=r"(r[3])
         : "r"(odd));
+}
+
+__device__ __forceinline__ int32_t max_byte(uint32_t w) {
+    return static_cast<int32_t>(max(max(w & 255u, (w >> 8) & 255u), max((w >> 16) & 255u, w >> 24)));
 }
 
 // 2^(b - 127) of byte i of w (b in 1..254).
