@@ -29,8 +29,9 @@ namespace yoco {
 namespace {
 
 constexpr int kChunk = 64;         // tokens of a chunk
-constexpr int kSlice = 64;         // value dims of a CTA
+constexpr int kSlice = 64;         // value dims of a single token's CTA
 constexpr int kChunkThreads = 256;
+constexpr uint64_t kRetWaitNs = 1000000000ull;  // before a wait gives up
 constexpr float kMinDecay = -80.f; // exp(-80) = 2e-35: less counts as this (and -inf stays a number)
 constexpr float kLn2Inv = 1.4426950408889634f;
 
@@ -243,13 +244,52 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
 }
 
 // -------------------------------------------------------------------- chunks
+//
+// One CTA walks the chunks of one (segment, head, slice of up to 128 value
+// dims) with the state transposed, S^T (value dims x key dims), as fp32
+// accumulators in tensor memory. A chunk of 64 tokens is four products of
+// 16-bit operands (128 value dims are the M side, so that the widest one has
+// the full 128 x 256 shape):
+//   P (tokens x tokens)  = q k^T
+//   O1^T (value x token) = S^T q^T            S^T as a bf16 copy in tensor memory
+//   O2^T                 = v^T P^T            P decayed, bf16, in shared memory
+//   S^T                 += (decayed v)^T k    after S^T was scaled by exp(L_C)
+// q, k and v lie in shared memory as blocks of 64 elements a row with the
+// 128-byte swizzle, which serve as K-major and as MN-major operands alike: no
+// operand is transposed by a thread. Roundings to bf16: P and the state's copy,
+// both below the rounding of the output; the decayed v as a sum of three bf16
+// terms (24 bits) where the state leaves the kernel, of two (16 bits) where it
+// only feeds later outputs of its segment.
+//
+// Without outputs (the states that segments add) v is decayed to the segment's
+// end, so that S^T is only ever added to.
 
-// Byte offset of 16-byte piece j of row r in a tile of ROW-byte rows, swizzled
-// so that the 8 rows of an ldmatrix fall in distinct banks.
-template <int ROW>
-__device__ __forceinline__ uint32_t tile_at(int r, int j) {
-    return static_cast<uint32_t>(r * ROW + ((j ^ (r & 7)) << 4));
-}
+constexpr int kVal = 128;        // value dims of a CTA (head_dim 64: half of them idle)
+constexpr int kMaxChunks = 512;  // of a segment
+constexpr int kBlockBytes = kChunk * 128;  // 64 tokens x 64 elements
+
+template <int D, bool OUT>
+struct RetShape {
+    static constexpr int VD = D < kVal ? D : kVal;             // value dims a CTA really has
+    static constexpr int NS = D / VD;                          // slices of a head
+    static constexpr int QB = OUT ? D / 64 * kBlockBytes : 0;
+    static constexpr int KB = D / 64 * kBlockBytes;
+    static constexpr int VB = VD / 64 * kBlockBytes;
+    static constexpr int STAGE = QB + KB + VB;
+    static constexpr int TERMS = 3 * VB;                       // decayed v, three terms
+    static constexpr int WBUF = OUT ? 1 : 2;                   // sets of terms
+    static constexpr int PB = OUT ? kBlockBytes : 0;
+    static constexpr int LB = 8 * (kChunk * 16 + 16);          // sums and factors of 8 chunks
+    static constexpr int TB = OUT ? 0 : kMaxChunks * 8;        // decay sums of a segment's chunks
+    // an operand of 128 rows over a block of 64 reads on into what follows: the
+    // last such block is a set of terms at head_dim 64, followed by 8 KiB and more
+    static constexpr int PAD = D == 64 ? kBlockBytes : 0;
+    static constexpr int SMEM = 2 * STAGE + WBUF * TERMS + PB + PAD + LB + TB + 1024;
+    // tensor memory columns: S^T, its bf16 copy, O1^T, O2^T (and P before it)
+    [[maybe_unused]] static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk, TCOLS = 512;
+    static_assert(!OUT || TO2 + kChunk <= TCOLS, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
 
 // 16 bytes global -> shared, or zeros.
 __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool there) {
@@ -258,307 +298,323 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
                  : "memory");
 }
 
-template <int D, bool OUT>
-struct RetShape {
-    static constexpr int ROWB = 2 * D;                       // bytes of a q or k row
-    static constexpr int QB = OUT ? kChunk * ROWB : 0;
-    static constexpr int KB = kChunk * ROWB;
-    static constexpr int VB = kChunk * kSlice * 2;
-    static constexpr int STAGE = QB + KB + VB;
-    static constexpr int SB = OUT ? D * kSlice * 2 : 0;      // the state in bf16
-    static constexpr int PB = OUT ? kChunk * kChunk * 2 : 0; // weights in bf16
-    static constexpr int LB = 8 * (kChunk * 16 + 16);        // sums and factors of 8 chunks
-    static constexpr int SMEM = 2 * STAGE + SB + PB + 3 * VB + LB + 1024;
-    static constexpr int CTAS = 2 * SMEM <= 224 * 1024 ? 2 : 1;  // of an SM
-    static constexpr int MT = D >= 128 ? D / 128 : 1;        // 16-row tiles of the state a warp holds
-    static constexpr int NTS = D >= 128 ? 8 : 4;             // its 8-column tiles
-};
+// Byte offset of 16-byte piece j of row t in swizzled blocks of 8 pieces a row.
+__device__ __forceinline__ uint32_t block_at(int t, int j) {
+    return static_cast<uint32_t>((j >> 3) * kBlockBytes + t * 128 + (((j & 7) ^ (t & 7)) << 4));
+}
 
-// One CTA walks the chunks of one (segment, head, 64 value dims); the state
-// slice [D][64] stays in the accumulator registers of its 8 warps. Products
-// are m16n8k16 bf16 with fp32 accumulators. Roundings to bf16: the weights P,
-// the state as an operand of q S (the state itself stays fp32), both below
-// the rounding of the output; exp(L_C - L_j) v_j as a sum of three bf16 terms
-// (24 bits) where the state leaves the kernel, of two (16 bits) where it only
-// feeds later outputs of its segment.
 template <int D, bool OUT>
-__global__ void __launch_bounds__(kChunkThreads, RetShape<D, OUT>::CTAS)
-    retention_chunks(const RetParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetParams p) {
     using S = RetShape<D, OUT>;
-    constexpr int NS = D / kSlice, MT = S::MT, NTS = S::NTS;
+    constexpr int NS = S::NS, VD = S::VD;
     extern __shared__ uint8_t ret_smem[];
+    __shared__ __align__(8) uint64_t bar_p, bar_o, bar_s[2];
+    __shared__ uint32_t tmem_base;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ret_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
-    const uint32_t s_state = base + 2 * S::STAGE, s_p = s_state + S::SB, s_vw = s_p + S::PB;
-    // of each of 8 chunks: 64 x {sum hi, sum lo, exp(L_t), exp(L_C - L_t)} in log2 units, then exp(L_C)
-    float4* const fac = reinterpret_cast<float4*>(smem + 2 * S::STAGE + S::SB + S::PB + 3 * S::VB);
+    constexpr int AT_W = 2 * S::STAGE, AT_P = AT_W + S::WBUF * S::TERMS, AT_F = AT_P + S::PB + S::PAD;
+    // of each of 8 chunks: 64 x {sum hi, sum lo, exp(L_t), exp(L_end - L_t)} in log2 units, then exp(L_C)
+    float4* const fac = reinterpret_cast<float4*>(smem + AT_F);
     float* const whole = reinterpret_cast<float*>(fac + 8 * kChunk);
+    double* const totals = reinterpret_cast<double*>(smem + AT_F + S::LB);  // !OUT
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int gl = lane >> 2, tq = lane & 3, mi = lane >> 3, rr = lane & 7;
-    // this warp's part of the state: rows row0.. (16 * MT), columns col0.. (8 * NTS)
-    const int row0 = D >= 128 ? warp * 16 * MT : (warp & 3) * 16;
-    const int col0 = D >= 128 ? 0 : (warp >> 2) * 32;
-    const int rb = warp & 3, cb = warp >> 2;  // 16 x 32 block of a 64 x 64 product
+    const int half = warp >> 2;                     // which half of the columns this warp takes
+    const int row = (warp & 3) * 32 + lane;         // its lane of tensor memory
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    if (tid == 0) {
+        mbar_init(&bar_p, 1);
+        mbar_init(&bar_o, 1);
+        mbar_init(&bar_s[0], 1);
+        mbar_init(&bar_s[1], 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) tmem_alloc(&tmem_base, S::TCOLS);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = tmem_base;
+    // phases of the barriers; state updates without outputs, of which two are under way
+    // at once, take the two of bar_s in turn
+    uint32_t ph_p = 0, ph_o = 0, ph_s[2] = {0, 0};
+    bool bad = false;                       // a wait has given up
+    auto wait = [&](uint64_t* bar, uint32_t& ph) {
+        if (!bad && !mbar_wait_bounded(bar, ph, kRetWaitNs)) bad = true;
+        ph ^= 1;
+    };
+    auto wait_update = [&](int32_t c) {
+        const int i = OUT ? 0 : c & 1;
+        if (i) wait(&bar_s[1], ph_s[1]);
+        else wait(&bar_s[0], ph_s[0]);
+    };
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
 
-    for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    for (int32_t item = blockIdx.x; item < items && !bad; item += gridDim.x) {
         const RetSeg sg = p.segs[item / (p.H * NS)];
         const bool last = sg.index == sg.count - 1;
         if (sg.count == 0 || (!OUT && last)) continue;
-        const int32_t h = item / NS % p.H, dv0 = item % NS * kSlice, hk = h / p.G;
+        const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
 
         auto load = [&](int32_t c) {  // chunk c into its stage
             const uint32_t st = base + (c & 1) * S::STAGE;
             const int32_t left = sg.tokens - c * kChunk;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
-            constexpr int J = D / 8;
+            constexpr int J = D / 8, JV = VD / 8;
 #pragma unroll
             for (int x = tid; x < kChunk * J; x += kChunkThreads) {
                 const int t = x / J, j = x % J;
                 const bool there = t < left;
-                const int64_t row = there ? t0 + t : t0;
+                const int64_t r = there ? t0 + t : t0;
                 if constexpr (OUT)
-                    cp_async_16_or_zero(st + tile_at<S::ROWB>(t, j), p.q + (row * p.H + h) * D + j * 8, there);
-                cp_async_16_or_zero(st + S::QB + tile_at<S::ROWB>(t, j), p.k + (row * H_kv + hk) * D + j * 8, there);
+                    cp_async_16_or_zero(st + block_at(t, j), p.q + (r * p.H + h) * D + j * 8, there);
+                cp_async_16_or_zero(st + S::QB + block_at(t, j), p.k + (r * H_kv + hk) * D + j * 8, there);
             }
 #pragma unroll
-            for (int x = tid; x < kChunk * 8; x += kChunkThreads) {
-                const int t = x >> 3, j = x & 7;
+            for (int x = tid; x < kChunk * JV; x += kChunkThreads) {
+                const int t = x / JV, j = x % JV;
                 const bool there = t < left;
-                const int64_t row = there ? t0 + t : t0;
-                cp_async_16_or_zero(st + S::QB + S::KB + tile_at<128>(t, j),
-                                    p.v + (row * H_kv + hk) * D + dv0 + j * 8, there);
+                const int64_t r = there ? t0 + t : t0;
+                cp_async_16_or_zero(st + S::QB + S::KB + block_at(t, j), p.v + (r * H_kv + hk) * D + dv0 + j * 8, there);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        __syncthreads();  // the previous item is done with the stages
+        __syncthreads();  // the previous item is done with shared and tensor memory
         load(0);
 
-        // the state before the segment
-        float s[MT][NTS][4];
-        {
+        // log decays of chunk cc (log2 units): lane l has tokens 2l and 2l + 1
+        auto decays = [&](int32_t cc, double& g0, double& g1) {
+            const int64_t t0 = sg.token + static_cast<int64_t>(cc) * kChunk;
+            const int32_t left = cc < chunks ? min(kChunk, sg.tokens - cc * kChunk) : 0;
+            constexpr double kLog2E = 1.4426950408889634074;
+            g0 = 2 * lane < left ? kLog2E * static_cast<double>(decay_of(p, t0 + 2 * lane, h)) : 0.0;
+            g1 = 2 * lane + 1 < left ? kLog2E * static_cast<double>(decay_of(p, t0 + 2 * lane + 1, h)) : 0.0;
+        };
+        if constexpr (OUT) {  // the state before the segment
             const float* src = nullptr;
-            if (OUT) {
-                const int32_t q = __ldg(p.qsl + sg.req + 1) - __ldg(p.qsl + sg.req);
-                if (sg.slot >= 0)
-                    src = p.slots + (static_cast<int64_t>(sg.slot) * p.H + h) * D * D + dv0;
-                else if (__ldg(p.seq_lens + sg.req) > q)
-                    src = p.state + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
+            const int32_t q = __ldg(p.qsl + sg.req + 1) - __ldg(p.qsl + sg.req);
+            if (sg.slot >= 0)
+                src = p.slots + (static_cast<int64_t>(sg.slot) * p.H + h) * D * D + dv0;
+            else if (__ldg(p.seq_lens + sg.req) > q)
+                src = p.state + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
+            if (row >= VD) src = nullptr;
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                const int c0 = half * (D / 2) + b * 32;
+                uint32_t x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    x[i] = src ? __float_as_uint(src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
+                tmem_st32(tm + lanes + S::TS + c0, x);
             }
+            tmem_st_wait();
+        } else {  // decay sums of the segment's chunks
+            for (int32_t cc = warp; cc < chunks; cc += 8) {
+                double g0, g1;
+                decays(cc, g0, g1);
+                double t = g0 + g1;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NTS; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float2 x = make_float2(0.f, 0.f);
-                        if (src)
-                            x = *reinterpret_cast<const float2*>(
-                                src + static_cast<int64_t>(row0 + m * 16 + gl + 8 * e) * D + col0 + n * 8 + 2 * tq);
-                        s[m][n][2 * e] = x.x;
-                        s[m][n][2 * e + 1] = x.y;
-                    }
+                for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+                if (lane == 0) totals[cc] = t;
+            }
+            __syncthreads();
         }
-        double decay_all = 0.0;  // warp 0: sum of the segment's log decays (log2 units)
+        bool pending = false;  // an update of the state is under way
 
         for (int32_t c = 0; c < chunks; ++c) {
             if ((c & 7) == 0) {  // running sums and factors of 8 chunks, one a warp
                 if (c) __syncthreads();
                 const int32_t cc = c + warp;
-                const int64_t t0 = sg.token + static_cast<int64_t>(cc) * kChunk;
-                const int32_t left = cc < chunks ? min(kChunk, sg.tokens - cc * kChunk) : 0;
-                // lane l has tokens 2l and 2l + 1
-                const double g0 = 2 * lane < left ? static_cast<double>(decay_of(p, t0 + 2 * lane, h)) : 0.0;
-                const double g1 = 2 * lane + 1 < left ? static_cast<double>(decay_of(p, t0 + 2 * lane + 1, h)) : 0.0;
+                double g0, g1;
+                decays(cc, g0, g1);
                 double sum = g0 + g1;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
                     const double x = __shfl_up_sync(0xffffffffu, sum, off);
                     if (lane >= off) sum += x;
                 }
-                constexpr double kLog2E = 1.4426950408889634074;
-                const double total = __shfl_sync(0xffffffffu, sum, 31) * kLog2E;
-                const double l1 = sum * kLog2E, l0 = (sum - g1) * kLog2E;
+                const double total = __shfl_sync(0xffffffffu, sum, 31);
+                double end = total;
+                if constexpr (!OUT) {  // to the end of the segment
+                    double t = 0.0;
+                    for (int32_t x = cc + 1 + lane; x < chunks; x += 32) t += totals[x];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+                    end += t;
+                }
                 auto factors = [&](double l) {
                     const float hi = static_cast<float>(l);
-                    return make_float4(hi, static_cast<float>(l - hi), exp2f(hi),
-                                       exp2f(static_cast<float>(total - l)));
+                    return make_float4(hi, static_cast<float>(l - hi), exp2f(hi), exp2f(static_cast<float>(end - l)));
                 };
-                fac[warp * kChunk + 2 * lane] = factors(l0);
-                fac[warp * kChunk + 2 * lane + 1] = factors(l1);
+                fac[warp * kChunk + 2 * lane] = factors(sum - g1);
+                fac[warp * kChunk + 2 * lane + 1] = factors(sum);
                 if (lane == 0) whole[warp] = exp2f(static_cast<float>(total));
-                if (!OUT && dv0 == 0) decay_all += total;
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            __syncthreads();  // chunk c is in shared memory; everyone is done with chunk c - 1
-            if (c + 1 < chunks) load(c + 1);
-            const uint32_t sq = base + (c & 1) * S::STAGE, sk = sq + S::QB, sv = sk + S::KB;
+            const uint32_t at = (c & 1) * S::STAGE;  // of the chunk's q, k, v
+            const uint32_t sq = base + at, sk = sq + S::QB, sv = sk + S::KB;
+            const uint32_t aw = AT_W + (S::WBUF == 2 ? (c & 1) * S::TERMS : 0);
             const float4* f = fac + (c & 7) * kChunk;
             const bool update = !OUT || last || c + 1 < chunks;
             const int terms = (!OUT || last) ? 3 : 2;
 
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            fence_proxy_async_smem();
+            if (OUT && pending) wait_update(c - 1);  // the state before this chunk is complete
+            tmem_fence_before();
+            bad = __syncthreads_or(bad);  // chunk c and its factors are in shared memory
+            if (bad) break;
+            tmem_fence_after();
             if constexpr (OUT) {
-                // weights P = (q k^T) exp(L_t - L_j), lower triangle: rows 16 rb.., columns 32 cb..
-                const int nt = min(4, 2 * (rb + 1) - 4 * cb);  // 8-column tiles that reach it
-                if (nt > 0) {
-                    float a[4][4];
+                if (c + 1 < chunks) load(c + 1);
+                if (tid == 0) {  // P = q k^T (128 rows: the upper 64 are not looked at)
 #pragma unroll
-                    for (int n = 0; n < 4; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a[n][e] = 0.f;
-#pragma unroll 4
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        uint32_t a0, a1, a2, a3, b[8];
-                        ldsm_x4(sq + tile_at<S::ROWB>(rb * 16 + (mi & 1) * 8 + rr, kk * 2 + (mi >> 1)), a0, a1, a2, a3);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-                            ldsm_x4(sk + tile_at<S::ROWB>(cb * 32 + n * 16 + (mi >> 1) * 8 + rr, kk * 2 + (mi & 1)),
-                                    b[4 * n], b[4 * n + 1], b[4 * n + 2], b[4 * n + 3]);
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) mma_bf16_16816(a[n], a0, a1, a2, a3, b[2 * n], b[2 * n + 1]);
+                        const uint32_t o = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+                        tmem_mma(tm + S::TO2, smem_operand(sq + o, 16, 1024), smem_operand(sk + o, 16, 1024),
+                                 bf16_product(128, kChunk, false, false), kk > 0);
                     }
-                    const int t0 = rb * 16 + gl;
-                    const float4 ft[2] = {f[t0], f[t0 + 8]};
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        if (n >= nt) continue;
-                        const int j = cb * 32 + n * 8 + 2 * tq;
-                        const float4 fj[2] = {f[j], f[j + 1]};
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int t = t0 + 8 * e;
-                            float w[2];
-#pragma unroll
-                            for (int u = 0; u < 2; ++u)
-                                w[u] = j + u <= t ? a[n][2 * e + u] * exp2_approx((ft[e].x - fj[u].x) + (ft[e].y - fj[u].y))
-                                                  : 0.f;
-                            const uint32_t at = s_p + tile_at<128>(t, cb * 4 + n) + 4 * tq;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(pack_bf16x2(w[0], w[1])) : "memory");
-                        }
-                    }
+                    tmem_commit(&bar_p);
                 }
-                // the state before the chunk, as an operand
+                __syncwarp();
+                // the state as a bf16 operand, then scaled by the chunk's decay
+                const float aC = whole[c & 7];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int b = 0; b < D / 64; ++b) {
+                    const int c0 = half * (D / 2) + b * 32;
+                    uint32_t x[32], y[16];
+                    tmem_ld32(tm + lanes + S::TS + c0, x);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int n = 0; n < NTS; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t at = s_state + tile_at<128>(row0 + m * 16 + gl + 8 * e, (col0 >> 3) + n) + 4 * tq;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at),
-                                         "r"(pack_bf16x2(s[m][n][2 * e], s[m][n][2 * e + 1]))
-                                         : "memory");
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        y[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                        x[2 * i] = __float_as_uint(__uint_as_float(x[2 * i]) * aC);
+                        x[2 * i + 1] = __float_as_uint(__uint_as_float(x[2 * i + 1]) * aC);
+                    }
+                    tmem_st16(tm + lanes + S::TC + c0 / 2, y);
+                    if (update) tmem_st32(tm + lanes + S::TS + c0, x);
+                }
             }
-            if (update) {  // exp(L_C - L_j) v_j in bf16 terms
+            if (update) {  // exp(L_end - L_j) v_j in bf16 terms
 #pragma unroll
-                for (int x = tid; x < kChunk * 8; x += kChunkThreads) {
-                    const int t = x >> 3, j = x & 7;
-                    const uint32_t at = tile_at<128>(t, j);
-                    const uint4 w = *reinterpret_cast<const uint4*>(smem + (sv - base) + at);
+                for (int x = tid; x < kChunk * (VD / 8); x += kChunkThreads) {
+                    const int t = x / (VD / 8), j = x % (VD / 8);
+                    const uint32_t o = block_at(t, j);
+                    const uint4 w = *reinterpret_cast<const uint4*>(smem + at + S::QB + S::KB + o);
                     const float fw = f[t].w;
                     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t o[3][4];
+                    uint32_t r[3][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float lo = bf16lo_to_f32(in[i]) * fw, hi = bf16hi_to_f32(in[i]) * fw;
 #pragma unroll
                         for (int u = 0; u < 3; ++u) {
-                            o[u][i] = pack_bf16x2(lo, hi);
-                            lo -= bf16lo_to_f32(o[u][i]);
-                            hi -= bf16hi_to_f32(o[u][i]);
+                            r[u][i] = pack_bf16x2(lo, hi);
+                            lo -= bf16lo_to_f32(r[u][i]);
+                            hi -= bf16hi_to_f32(r[u][i]);
                         }
                     }
 #pragma unroll
                     for (int u = 0; u < 3; ++u)
-                        *reinterpret_cast<uint4*>(smem + (s_vw - base) + u * S::VB + at) =
-                            make_uint4(o[u][0], o[u][1], o[u][2], o[u][3]);
+                        *reinterpret_cast<uint4*>(smem + aw + u * S::VB + o) =
+                            make_uint4(r[u][0], r[u][1], r[u][2], r[u][3]);
                 }
             }
-            __syncthreads();
+            fence_proxy_async_smem();
+            if constexpr (OUT) tmem_st_wait();
+            tmem_fence_before();
+            __syncthreads();  // the state's copy and the terms are complete
             if constexpr (OUT) {
-                float o[4][4];
+                if (tid == 0) {  // O1^T = S^T q^T
+                    tmem_fence_after();
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-#pragma unroll 4
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t a0, a1, a2, a3, b[8];
-                    ldsm_x4(sq + tile_at<S::ROWB>(rb * 16 + (mi & 1) * 8 + rr, kk * 2 + (mi >> 1)), a0, a1, a2, a3);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        ldsm_x4_trans(s_state + tile_at<128>(kk * 16 + (mi & 1) * 8 + rr, cb * 4 + n * 2 + (mi >> 1)),
-                                      b[4 * n], b[4 * n + 1], b[4 * n + 2], b[4 * n + 3]);
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) mma_bf16_16816(o[n], a0, a1, a2, a3, b[2 * n], b[2 * n + 1]);
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tmem_mma_ta(tm + S::TO1, tm + S::TC + kk * 8,
+                                    smem_operand(sq + (kk >> 2) * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                    bf16_product(128, kChunk, false, false), kk > 0);
                 }
-                const float e0 = f[rb * 16 + gl].z, e1 = f[rb * 16 + gl + 8].z;
+                __syncwarp();
+                wait(&bar_p, ph_p);
+                tmem_fence_after();
+                if (row < kChunk) {  // warps 0, 1, 4, 5: weights of token `row`, 32 earlier tokens
+                    uint32_t x[32];
+                    tmem_ld32(tm + lanes + S::TO2 + half * 32, x);
+                    tmem_ld_wait();
+                    const float4 ft = f[row];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    o[n][0] *= e0;
-                    o[n][1] *= e0;
-                    o[n][2] *= e1;
-                    o[n][3] *= e1;
-                }
-                for (int kk = 0; kk <= rb; ++kk) {  // later columns of P are zero for these rows
-                    uint32_t a0, a1, a2, a3, b[8];
-                    ldsm_x4(s_p + tile_at<128>(rb * 16 + (mi & 1) * 8 + rr, kk * 2 + (mi >> 1)), a0, a1, a2, a3);
+                    for (int q8 = 0; q8 < 4; ++q8) {
+                        uint32_t w[4];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
-                        ldsm_x4_trans(sv + tile_at<128>(kk * 16 + (mi & 1) * 8 + rr, cb * 4 + n * 2 + (mi >> 1)),
-                                      b[4 * n], b[4 * n + 1], b[4 * n + 2], b[4 * n + 3]);
+                        for (int i = 0; i < 4; ++i) {
+                            float y[2];
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) mma_bf16_16816(o[n], a0, a1, a2, a3, b[2 * n], b[2 * n + 1]);
-                }
-                const int32_t left = sg.tokens - c * kChunk;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = rb * 16 + gl + 8 * e;
-                    if (t >= left) continue;
-                    __nv_bfloat16* dst = p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + t) * p.H + h) * D + dv0 +
-                                         cb * 32 + 2 * tq;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                            pack_bf16x2(o[n][2 * e] * p.scale, o[n][2 * e + 1] * p.scale);
-                }
-            }
-            if (update) {
-                const float aC = whole[c & 7];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int n = 0; n < NTS; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[m][n][e] *= aC;
-#pragma unroll 1
-                for (int kk = 0; kk < kChunk / 16; ++kk) {
-                    uint32_t a[MT][4];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-                        ldsm_x4_trans(sk + tile_at<S::ROWB>(kk * 16 + (mi >> 1) * 8 + rr, (row0 >> 3) + m * 2 + (mi & 1)),
-                                      a[m][0], a[m][1], a[m][2], a[m][3]);
-                    for (int u = 0; u < terms; ++u) {
-#pragma unroll
-                        for (int n = 0; n < NTS / 2; ++n) {
-                            uint32_t b[4];
-                            ldsm_x4_trans(s_vw + u * S::VB +
-                                              tile_at<128>(kk * 16 + (mi & 1) * 8 + rr, (col0 >> 3) + n * 2 + (mi >> 1)),
-                                          b[0], b[1], b[2], b[3]);
-#pragma unroll
-                            for (int m = 0; m < MT; ++m) {
-                                mma_bf16_16816(s[m][2 * n], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
-                                mma_bf16_16816(s[m][2 * n + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+                            for (int u = 0; u < 2; ++u) {
+                                const int j = half * 32 + q8 * 8 + 2 * i + u;
+                                const float2 fj = *reinterpret_cast<const float2*>(f + j);
+                                y[u] = j <= row ? __uint_as_float(x[q8 * 8 + 2 * i + u]) *
+                                                      exp2_approx((ft.x - fj.x) + (ft.y - fj.y))
+                                                : 0.f;
                             }
+                            w[i] = pack_bf16x2(y[0], y[1]);
                         }
+                        *reinterpret_cast<uint4*>(smem + AT_P + block_at(row, half * 4 + q8)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                fence_proxy_async_smem();
+                tmem_fence_before();
+                __syncthreads();  // P is in shared memory, its columns are free
+            }
+            if (tid == 0) {
+                tmem_fence_after();
+                if constexpr (OUT) {  // O2^T = v^T P^T
+#pragma unroll
+                    for (int kk = 0; kk < kChunk / 16; ++kk)
+                        tmem_mma(tm + S::TO2, smem_operand(sv + kk * 2048, kBlockBytes, 1024),
+                                 smem_operand(base + AT_P + kk * 32, 16, 1024), bf16_product(128, kChunk, true, false),
+                                 kk > 0);
+                    tmem_commit(&bar_o);
+                }
+                if (update) {  // S^T += (decayed v)^T k
+                    for (int u = 0; u < terms; ++u)
+#pragma unroll
+                        for (int kk = 0; kk < kChunk / 16; ++kk)
+                            tmem_mma(tm + S::TS, smem_operand(base + aw + u * S::VB + kk * 2048, kBlockBytes, 1024),
+                                     smem_operand(sk + kk * 2048, kBlockBytes, 1024), bf16_product(128, D, true, true),
+                                     OUT || c > 0 || u > 0 || kk > 0);
+                    tmem_commit(&bar_s[OUT ? 0 : c & 1]);
+                }
+            }
+            __syncwarp();
+            if constexpr (OUT) {
+                pending = update;
+                wait(&bar_o, ph_o);
+                tmem_fence_after();
+                uint32_t a[32], b[32];
+                tmem_ld32(tm + lanes + S::TO1 + half * 32, a);
+                tmem_ld32(tm + lanes + S::TO2 + half * 32, b);
+                tmem_ld_wait();
+                const int32_t left = sg.tokens - c * kChunk - half * 32;
+                if (row < VD) {  // a warp's 32 lanes are 64 bytes of each token's row
+                    __nv_bfloat16* dst =
+                        p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + half * 32) * p.H + h) * D + dv0 + row;
+#pragma unroll
+                    for (int t = 0; t < 32; ++t)
+                        if (t < left)
+                            dst[static_cast<int64_t>(t) * p.H * D] = __float2bfloat16_rn(
+                                p.scale * fmaf(f[half * 32 + t].z, __uint_as_float(a[t]), __uint_as_float(b[t])));
+                }
+            } else {
+                // the products of the chunk before are done with its stage and terms
+                if (pending) wait_update(c - 1);
+                pending = true;
+                if (c + 1 < chunks) load(c + 1);
             }
         }
+        if (pending) wait_update(chunks - 1);
+        bad = __syncthreads_or(bad);
+        if (bad) break;
+        tmem_fence_after();
         // the state after the segment
         float* dst = nullptr;
         if (!OUT)
@@ -567,35 +623,41 @@ __global__ void __launch_bounds__(kChunkThreads, RetShape<D, OUT>::CTAS)
             dst = p.state_out + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
         if (dst) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int b = 0; b < D / 64; ++b) {
+                const int c0 = half * (D / 2) + b * 32;
+                uint32_t x[32];
+                tmem_ld32(tm + lanes + S::TS + c0, x);
+                tmem_ld_wait();
+                if (row < VD)
 #pragma unroll
-                for (int n = 0; n < NTS; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float2*>(dst + static_cast<int64_t>(row0 + m * 16 + gl + 8 * e) * D + col0 +
-                                                   n * 8 + 2 * tq) = make_float2(s[m][n][2 * e], s[m][n][2 * e + 1]);
-        }
-        if (!OUT && dv0 == 0) {  // every warp has the sums of its own chunks
-            __syncthreads();
-            double* all = reinterpret_cast<double*>(fac);
-            if (lane == 0) all[warp] = decay_all;
-            __syncthreads();
-            if (tid == 0) {
-                double t = 0.0;
-                for (int w = 0; w < 8; ++w) t += all[w];
-                p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(static_cast<float>(t));
+                    for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
             }
         }
+        if (!OUT && dv0 == 0 && warp == 0) {  // the segment's decay
+            double t = 0.0;
+            for (int32_t x = lane; x < chunks; x += 32) t += totals[x];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+            if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(static_cast<float>(t));
+        }
+        tmem_fence_before();
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (bad && tid == 0) set_err(p.err, YOCO_DEVERR_TIMEOUT);
+    if (warp == 0) tmem_dealloc(tm, S::TCOLS);
 }
 
 // ------------------------------------------------------------------ host side
 
 constexpr int kMinSegment = 256;  // tokens
+constexpr int kMaxSegment = kMaxChunks * kChunk;
 
 // Segments to aim for: about two CTAs for every SM over heads and slices.
 int64_t ret_target(int H, int D) {
-    const int64_t units = static_cast<int64_t>(H) * (D / kSlice);
+    const int64_t units = static_cast<int64_t>(H) * (D > kVal ? D / kVal : 1);
     const int64_t n = (2ll * device_sm_count() + units - 1) / units;
     return n < 1 ? 1 : n;
 }
@@ -612,6 +674,7 @@ RetPlan ret_plan(int64_t R, int64_t T, int64_t max_q, int H, int D) {
     const int64_t target = ret_target(H, D);
     int64_t seg = ((T + target - 1) / target + kChunk - 1) / kChunk * kChunk;
     if (seg < kMinSegment) seg = kMinSegment;
+    if (seg > kMaxSegment) seg = kMaxSegment;
     x.seg_tokens = seg;
     // whole segments, and at most one shorter one for each request of two tokens or more
     const int64_t shorter = R < T / 2 ? R : T / 2;
@@ -625,7 +688,9 @@ RetPlan ret_plan(int64_t R, int64_t T, int64_t max_q, int H, int D) {
 RetPlan ret_sizes(int64_t R, int64_t T, int64_t max_q, int H, int D) {
     RetPlan x = ret_plan(R, T, max_q, H, D);
     if (x.seg_tokens == 0) return x;
-    const int64_t target = ret_target(H, D), whole = T / kMinSegment < target ? T / kMinSegment : target;
+    int64_t whole = ret_target(H, D);
+    if (whole < T / kMaxSegment) whole = T / kMaxSegment;
+    if (whole > T / kMinSegment) whole = T / kMinSegment;
     const int64_t segs = whole + (R < T / 2 ? R : T / 2), slots = max_q > kMinSegment ? 2 * whole : 0;
     x.list_bytes = (16 + static_cast<size_t>(segs) * sizeof(RetSeg) + 255) & ~static_cast<size_t>(255);
     x.decay_bytes = (static_cast<size_t>(slots) * H * 4 + 255) & ~static_cast<size_t>(255);
@@ -656,14 +721,14 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = ret_smem_attr(retention_chunks<D, false>, RetShape<D, false>::SMEM, done_add);
     if (e != cudaSuccess) return e;
     retention_plan<<<1, 1024, 0, s>>>(p);
-    const int64_t sms = device_sm_count(), items = static_cast<int64_t>(p.max_segs) * p.H * NS;
-    auto grid = [&](int64_t per) { return static_cast<unsigned>(items < sms * per ? items : sms * per); };
+    const int64_t sms = device_sm_count(), items = static_cast<int64_t>(p.max_segs) * p.H * RetShape<D, true>::NS;
+    const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);  // one CTA an SM
     if (p.max_slots > 0) {
-        retention_chunks<D, false><<<grid(RetShape<D, false>::CTAS), kChunkThreads, RetShape<D, false>::SMEM, s>>>(p);
+        retention_chunks<D, false><<<grid, kChunkThreads, RetShape<D, false>::SMEM, s>>>(p);
         const int64_t parts = static_cast<int64_t>(p.max_segs) * p.H * (D * D / 1024);
         retention_scan<D><<<static_cast<unsigned>(parts < 16 * sms ? parts : 16 * sms), 256, 0, s>>>(p);
     }
-    retention_chunks<D, true><<<grid(RetShape<D, true>::CTAS), kChunkThreads, RetShape<D, true>::SMEM, s>>>(p);
+    retention_chunks<D, true><<<grid, kChunkThreads, RetShape<D, true>::SMEM, s>>>(p);
     return cudaGetLastError();
 }
 
