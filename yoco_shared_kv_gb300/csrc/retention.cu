@@ -32,6 +32,9 @@ constexpr int kChunk = 64;         // tokens of a chunk
 constexpr int kSlice = 64;         // value dims of a single token's CTA
 constexpr int kChunkThreads = 256;
 constexpr uint64_t kRetWaitNs = 1000000000ull;  // before a wait gives up
+constexpr int kMaxChunks = 512;                 // of a segment
+constexpr int kMaxSegment = kMaxChunks * kChunk;
+constexpr int kChooseReqs = 4096;               // with more requests segments take the shortest length
 constexpr float kMinDecay = -80.f; // exp(-80) = 2e-35: less counts as this (and -inf stays a number)
 constexpr float kLn2Inv = 1.4426950408889634f;
 
@@ -51,7 +54,7 @@ struct RetParams {
     int32_t H, G;              // heads, heads per k/v head
     int32_t by_token;          // decay has a row for each token
     float scale;
-    int32_t seg_tokens;        // tokens of a segment, a multiple of kChunk
+    int32_t seg_tokens;        // tokens of a segment at least, a multiple of kChunk
     int32_t max_segs, max_slots;
     // workspace
     struct RetSeg* segs;
@@ -104,7 +107,12 @@ __global__ void __launch_bounds__(256) retention_step(const RetParams p) {
     int32_t q0, q1, where;
     bool fresh;
     const bool ok = ret_request(p, r, h == 0 && slice == 0 && threadIdx.x == 0, q0, q1, where, fresh);
-    if (!ok || q1 - q0 != 1) return;
+    // Where it was launched beside the segments' pass, this kernel ends after that one (what
+    // follows it in the stream waits for this one alone).
+    if (!ok || q1 - q0 != 1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int c = threadIdx.x & 15, rg = threadIdx.x >> 4;
     const int64_t tok = q0;
     const int32_t hk = h / p.G, H_kv = p.H / p.G;
@@ -151,14 +159,63 @@ __global__ void __launch_bounds__(256) retention_step(const RetParams p) {
         for (int g = 0; g < 16; ++g) t += f[g * kSlice];
         p.out[(tok * p.H + h) * D + slice * kSlice + threadIdx.x] = __float2bfloat16_rn(t * p.scale);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ segments
 
-// One CTA: segments of every request of two tokens or more, in request order.
-__global__ void __launch_bounds__(1024) retention_plan(const RetParams p) {
+// Time of both chunk passes, in eighths of a chunk with outputs, if requests are cut into
+// `segs` segments of up to `chunks` chunks (`cut` of them not a request's last, `all` chunks
+// together) over `units` heads and slices: rounds of whole segments on all SMs, or the work
+// evenly spread and one segment more, whichever is less. A segment costs about 4 chunks
+// beside its own; a chunk without outputs half of one with.
+__device__ __forceinline__ int64_t pass_time(int64_t segs, int64_t cut, int64_t all, int64_t chunks,
+                                             int64_t units, int64_t sms) {
+    auto one = [&](int64_t n, int64_t work) {
+        const int64_t rounds = (n * units + sms - 1) / sms * (chunks + 4);
+        const int64_t even = (work + 4 * n) * units / sms + chunks + 4;
+        return rounds < even ? rounds : even;
+    };
+    return 8 * one(segs, all) + (cut ? 4 * one(cut, cut * chunks) : 0);
+}
+
+// One CTA: segments of every request of two tokens or more, in request order. Their length
+// is the best of 32, from the shortest that the workspace has room for upwards.
+__global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t units, int32_t sms) {
     __shared__ int32_t tot[2][32];
+    __shared__ int64_t cost[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (p.max_slots > 0 && p.num_reqs <= kChooseReqs) {
+        const float grown = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(warp) / 6.f);
+        const int32_t seg = min((static_cast<int32_t>(fminf(grown, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
+        int32_t segs = 0, slots = 0, cut = 0, all = 0, longest = 0;
+        for (int32_t r = lane; r < p.num_reqs; r += 32) {
+            int32_t q0, q1, where;
+            bool fresh;
+            if (!ret_request(p, r, false, q0, q1, where, fresh) || q1 - q0 < 2) continue;
+            const int32_t n = (q1 - q0 + seg - 1) / seg;
+            segs += n;
+            if (n > 1) slots += n;
+            cut += n - 1;
+            all += (q1 - q0 + kChunk - 1) / kChunk;
+            longest = max(longest, min(q1 - q0, seg));
+        }
+        segs = __reduce_add_sync(0xffffffffu, segs);
+        slots = __reduce_add_sync(0xffffffffu, slots);
+        cut = __reduce_add_sync(0xffffffffu, cut);
+        all = __reduce_add_sync(0xffffffffu, all);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0)
+            cost[warp] = segs > p.max_segs || slots > p.max_slots
+                             ? INT64_MAX
+                             : pass_time(segs, cut, all, (longest + kChunk - 1) / kChunk, units, sms);
+        __syncthreads();
+        int best = 0;
+        for (int i = 1; i < 32; ++i)
+            if (cost[i] < cost[best]) best = i;
+        const float chosen = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(best) / 6.f);
+        p.seg_tokens = min((static_cast<int32_t>(fminf(chosen, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
+    }
     int64_t seg0 = 0, slot0 = 0;
     for (int32_t base = 0; base < p.num_reqs; base += 1024) {
         const int32_t r = base + tid;
@@ -230,15 +287,26 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
         float* slot = p.slots + (static_cast<int64_t>(s.base) * p.H + h) * D * D + at;
         const int64_t stride = static_cast<int64_t>(p.H) * D * D;
         *reinterpret_cast<float4*>(slot) = x;
-        for (int32_t i = 0; i + 1 < s.count; ++i) {
-            slot += stride;
-            const float a = p.seg_decay[static_cast<int64_t>(s.base + i) * p.H + h];
-            const float4 y = *reinterpret_cast<const float4*>(slot);
-            x.x = fmaf(a, x.x, y.x);
-            x.y = fmaf(a, x.y, y.y);
-            x.z = fmaf(a, x.z, y.z);
-            x.w = fmaf(a, x.w, y.w);
-            *reinterpret_cast<float4*>(slot) = x;
+        constexpr int AHEAD = 8;  // loads do not wait for the sums
+        for (int32_t i = 0; i + 1 < s.count; i += AHEAD) {
+            float4 y[AHEAD];
+            float a[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i + u + 1 < s.count) {
+                    y[u] = *reinterpret_cast<const float4*>(slot + (u + 1) * stride);
+                    a[u] = p.seg_decay[static_cast<int64_t>(s.base + i + u) * p.H + h];
+                }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+                if (i + u + 1 < s.count) {
+                    x.x = fmaf(a[u], x.x, y[u].x);
+                    x.y = fmaf(a[u], x.y, y[u].y);
+                    x.z = fmaf(a[u], x.z, y[u].z);
+                    x.w = fmaf(a[u], x.w, y[u].w);
+                    *reinterpret_cast<float4*>(slot + (u + 1) * stride) = x;
+                }
+            slot += AHEAD * stride;
         }
     }
 }
@@ -265,7 +333,6 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
 // end, so that S^T is only ever added to.
 
 constexpr int kVal = 128;        // value dims of a CTA (head_dim 64: half of them idle)
-constexpr int kMaxChunks = 512;  // of a segment
 constexpr int kBlockBytes = kChunk * 128;  // 64 tokens x 64 elements
 
 template <int D, bool OUT>
@@ -277,14 +344,15 @@ struct RetShape {
     static constexpr int VB = VD / 64 * kBlockBytes;
     static constexpr int STAGE = QB + KB + VB;
     static constexpr int TERMS = 3 * VB;                       // decayed v, three terms
-    static constexpr int WBUF = OUT ? 1 : 2;                   // sets of terms
+    static constexpr int WBUF = OUT || D == 256 ? 1 : 2;       // sets of terms
+    static constexpr int STAGES = OUT ? 2 : 3;
     static constexpr int PB = OUT ? kBlockBytes : 0;
     static constexpr int LB = 8 * (kChunk * 16 + 16);          // sums and factors of 8 chunks
     static constexpr int TB = OUT ? 0 : kMaxChunks * 8;        // decay sums of a segment's chunks
     // an operand of 128 rows over a block of 64 reads on into what follows: the
     // last such block is a set of terms at head_dim 64, followed by 8 KiB and more
     static constexpr int PAD = D == 64 ? kBlockBytes : 0;
-    static constexpr int SMEM = 2 * STAGE + WBUF * TERMS + PB + PAD + LB + TB + 1024;
+    static constexpr int SMEM = STAGES * STAGE + WBUF * TERMS + PB + PAD + LB + TB + 1024;
     // tensor memory columns: S^T, its bf16 copy, O1^T, O2^T (and P before it)
     [[maybe_unused]] static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk, TCOLS = 512;
     static_assert(!OUT || TO2 + kChunk <= TCOLS, "tensor memory");
@@ -313,10 +381,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ret_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
-    constexpr int AT_W = 2 * S::STAGE, AT_P = AT_W + S::WBUF * S::TERMS, AT_F = AT_P + S::PB + S::PAD;
-    // of each of 8 chunks: 64 x {sum hi, sum lo, exp(L_t), exp(L_end - L_t)} in log2 units, then exp(L_C)
-    float4* const fac = reinterpret_cast<float4*>(smem + AT_F);
-    float* const whole = reinterpret_cast<float*>(fac + 8 * kChunk);
+    constexpr int AT_W = S::STAGES * S::STAGE, AT_P = AT_W + S::WBUF * S::TERMS, AT_F = AT_P + S::PB + S::PAD;
+    // of each of 8 chunks: sums of 64 tokens (high and low parts, log2 units), exp(L_t) and
+    // exp(L_end - L_t); then exp(L_C)
+    float* const fac = reinterpret_cast<float*>(smem + AT_F);
+    float* const whole = fac + 8 * 4 * kChunk;
     double* const totals = reinterpret_cast<double*>(smem + AT_F + S::LB);  // !OUT
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int half = warp >> 2;                     // which half of the columns this warp takes
@@ -334,6 +403,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
     __syncthreads();
     tmem_fence_after();
     const uint32_t tm = tmem_base;
+    // single tokens may run beside the segments' pass
+    if constexpr (!OUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // phases of the barriers; state updates without outputs, of which two are under way
     // at once, take the two of bar_s in turn
     uint32_t ph_p = 0, ph_o = 0, ph_s[2] = {0, 0};
@@ -358,7 +429,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
 
         auto load = [&](int32_t c) {  // chunk c into its stage
-            const uint32_t st = base + (c & 1) * S::STAGE;
+            const uint32_t st = base + c % S::STAGES * S::STAGE;
             const int32_t left = sg.tokens - c * kChunk;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
             constexpr int J = D / 8, JV = VD / 8;
@@ -382,6 +453,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
         };
         __syncthreads();  // the previous item is done with shared and tensor memory
         load(0);
+        if (S::STAGES == 3 && chunks > 1) load(1);
 
         // log decays of chunk cc (log2 units): lane l has tokens 2l and 2l + 1
         auto decays = [&](int32_t cc, double& g0, double& g1) {
@@ -443,28 +515,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                     for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
                     end += t;
                 }
-                auto factors = [&](double l) {
-                    const float hi = static_cast<float>(l);
-                    return make_float4(hi, static_cast<float>(l - hi), exp2f(hi), exp2f(static_cast<float>(end - l)));
+                auto put = [&](int i, float x, float y) {
+                    *reinterpret_cast<float2*>(fac + (warp * 4 + i) * kChunk + 2 * lane) = make_float2(x, y);
                 };
-                fac[warp * kChunk + 2 * lane] = factors(sum - g1);
-                fac[warp * kChunk + 2 * lane + 1] = factors(sum);
+                const double l0 = sum - g1, l1 = sum;
+                const float h0 = static_cast<float>(l0), h1 = static_cast<float>(l1);
+                if constexpr (OUT) {
+                    put(0, h0, h1);
+                    put(1, static_cast<float>(l0 - h0), static_cast<float>(l1 - h1));
+                    put(2, exp2f(h0), exp2f(h1));
+                }
+                put(3, exp2f(static_cast<float>(end - l0)), exp2f(static_cast<float>(end - l1)));
                 if (lane == 0) whole[warp] = exp2f(static_cast<float>(total));
             }
-            const uint32_t at = (c & 1) * S::STAGE;  // of the chunk's q, k, v
+            const uint32_t at = c % S::STAGES * S::STAGE;  // of the chunk's q, k, v
             const uint32_t sq = base + at, sk = sq + S::QB, sv = sk + S::KB;
             const uint32_t aw = AT_W + (S::WBUF == 2 ? (c & 1) * S::TERMS : 0);
-            const float4* f = fac + (c & 7) * kChunk;
+            const float* f = fac + (c & 7) * 4 * kChunk;
             const bool update = !OUT || last || c + 1 < chunks;
             const int terms = (!OUT || last) ? 3 : 2;
 
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if (S::STAGES == 3 && c + 1 < chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 0;" ::: "memory");
             fence_proxy_async_smem();
-            if (OUT && pending) wait_update(c - 1);  // the state before this chunk is complete
+            // the state before this chunk is complete (with one set of terms: they are free)
+            if (S::WBUF == 1 && pending) wait_update(c - 1);
             tmem_fence_before();
             bad = __syncthreads_or(bad);  // chunk c and its factors are in shared memory
             if (bad) break;
             tmem_fence_after();
+            if (!OUT && S::WBUF == 1 && c + 2 < chunks) load(c + 2);
             if constexpr (OUT) {
                 if (c + 1 < chunks) load(c + 1);
                 if (tid == 0) {  // P = q k^T (128 rows: the upper 64 are not looked at)
@@ -501,7 +581,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                     const int t = x / (VD / 8), j = x % (VD / 8);
                     const uint32_t o = block_at(t, j);
                     const uint4 w = *reinterpret_cast<const uint4*>(smem + at + S::QB + S::KB + o);
-                    const float fw = f[t].w;
+                    const float fw = f[3 * kChunk + t];
                     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
                     uint32_t r[3][4];
 #pragma unroll
@@ -540,22 +620,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                     uint32_t x[32];
                     tmem_ld32(tm + lanes + S::TO2 + half * 32, x);
                     tmem_ld_wait();
-                    const float4 ft = f[row];
+                    const float th = f[row], tl = f[kChunk + row];
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8) {
+                        const int j0 = half * 32 + q8 * 8;
                         uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float y[2];
+                        for (int v = 0; v < 2; ++v) {
+                            const float4 jh = *reinterpret_cast<const float4*>(f + j0 + 4 * v);
+                            const float4 jl = *reinterpret_cast<const float4*>(f + kChunk + j0 + 4 * v);
+                            const float d[4] = {(th - jh.x) + (tl - jl.x), (th - jh.y) + (tl - jl.y),
+                                                (th - jh.z) + (tl - jl.z), (th - jh.w) + (tl - jl.w)};
+                            float y[4];
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int j = half * 32 + q8 * 8 + 2 * i + u;
-                                const float2 fj = *reinterpret_cast<const float2*>(f + j);
-                                y[u] = j <= row ? __uint_as_float(x[q8 * 8 + 2 * i + u]) *
-                                                      exp2_approx((ft.x - fj.x) + (ft.y - fj.y))
-                                                : 0.f;
-                            }
-                            w[i] = pack_bf16x2(y[0], y[1]);
+                            for (int i = 0; i < 4; ++i)
+                                y[i] = j0 + 4 * v + i <= row
+                                           ? __uint_as_float(x[q8 * 8 + 4 * v + i]) * exp2_approx(d[i])
+                                           : 0.f;
+                            w[2 * v] = pack_bf16x2(y[0], y[1]);
+                            w[2 * v + 1] = pack_bf16x2(y[2], y[3]);
                         }
                         *reinterpret_cast<uint4*>(smem + AT_P + block_at(row, half * 4 + q8)) =
                             make_uint4(w[0], w[1], w[2], w[3]);
@@ -595,20 +678,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                 tmem_ld32(tm + lanes + S::TO2 + half * 32, b);
                 tmem_ld_wait();
                 const int32_t left = sg.tokens - c * kChunk - half * 32;
-                if (row < VD) {  // a warp's 32 lanes are 64 bytes of each token's row
-                    __nv_bfloat16* dst =
-                        p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + half * 32) * p.H + h) * D + dv0 + row;
+                // Two lanes exchange, so that each writes two value dims of every other token: a
+                // warp's 32 lanes are 64 bytes of two tokens' rows.
+                const bool odd = lane & 1;
+                uint32_t* dst = reinterpret_cast<uint32_t*>(
+                    p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + half * 32 + odd) * p.H + h) * D + dv0 +
+                    (row & ~1));
+                const float* et = f + 2 * kChunk + half * 32;
 #pragma unroll
-                    for (int t = 0; t < 32; ++t)
-                        if (t < left)
-                            dst[static_cast<int64_t>(t) * p.H * D] = __float2bfloat16_rn(
-                                p.scale * fmaf(f[half * 32 + t].z, __uint_as_float(a[t]), __uint_as_float(b[t])));
+                for (int t = 0; t < 32; t += 2) {
+                    const float2 e2 = *reinterpret_cast<const float2*>(et + t);
+                    const float y0 = p.scale * fmaf(e2.x, __uint_as_float(a[t]), __uint_as_float(b[t]));
+                    const float y1 = p.scale * fmaf(e2.y, __uint_as_float(a[t + 1]), __uint_as_float(b[t + 1]));
+                    const float z = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+                    if (row < VD && t + odd < left)
+                        dst[static_cast<int64_t>(t) * p.H * (D / 2)] = odd ? pack_bf16x2(z, y1) : pack_bf16x2(y0, z);
                 }
             } else {
                 // the products of the chunk before are done with its stage and terms
-                if (pending) wait_update(c - 1);
+                if (S::WBUF == 2 && pending) wait_update(c - 1);
                 pending = true;
-                if (c + 1 < chunks) load(c + 1);
+                if (S::WBUF == 2 && c + 2 < chunks) load(c + 2);
             }
         }
         if (pending) wait_update(chunks - 1);
@@ -653,7 +743,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
 // ------------------------------------------------------------------ host side
 
 constexpr int kMinSegment = 256;  // tokens
-constexpr int kMaxSegment = kMaxChunks * kChunk;
 
 // Segments to aim for: about two CTAs for every SM over heads and slices.
 int64_t ret_target(int H, int D) {
@@ -712,19 +801,36 @@ cudaError_t ret_smem_attr(K kernel, int bytes, unsigned long long& done) {
 
 template <int D>
 cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
-    constexpr int NS = D / kSlice;
-    retention_step<D><<<static_cast<unsigned>(static_cast<int64_t>(p.num_reqs) * p.H * NS), 256, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.seg_tokens == 0) return e;
+    const unsigned steps = static_cast<unsigned>(static_cast<int64_t>(p.num_reqs) * p.H * (D / kSlice));
+    const bool cut = p.seg_tokens > 0 && p.max_slots > 0;
+    cudaError_t e;
+    if (!cut) {
+        retention_step<D><<<steps, 256, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess || p.seg_tokens == 0) return e;
+    }
     static unsigned long long done_out = 0, done_add = 0;
     e = ret_smem_attr(retention_chunks<D, true>, RetShape<D, true>::SMEM, done_out);
     if (e == cudaSuccess) e = ret_smem_attr(retention_chunks<D, false>, RetShape<D, false>::SMEM, done_add);
     if (e != cudaSuccess) return e;
-    retention_plan<<<1, 1024, 0, s>>>(p);
-    const int64_t sms = device_sm_count(), items = static_cast<int64_t>(p.max_segs) * p.H * RetShape<D, true>::NS;
+    const int sms = device_sm_count(), units = p.H * RetShape<D, true>::NS;
+    const int64_t items = static_cast<int64_t>(p.max_segs) * units;
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);  // one CTA an SM
-    if (p.max_slots > 0) {
+    retention_plan<<<1, 1024, 0, s>>>(p, units, sms);
+    if (cut) {
         retention_chunks<D, false><<<grid, kChunkThreads, RetShape<D, false>::SMEM, s>>>(p);
+        // single tokens: bound by HBM, they run beside the segments' products
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(steps);
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, retention_step<D>, p);
+        if (e != cudaSuccess) return e;
         const int64_t parts = static_cast<int64_t>(p.max_segs) * p.H * (D * D / 1024);
         retention_scan<D><<<static_cast<unsigned>(parts < 16 * sms ? parts : 16 * sms), 256, 0, s>>>(p);
     }
