@@ -217,10 +217,12 @@ __device__ __forceinline__ void tmem_fence_before() {
 __device__ __forceinline__ void tmem_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void tmem_commit(uint64_t* bar) {  // a whole warp; one lane issues
+    asm volatile(
+        "{ .reg .pred q; elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(
+            smem_u32(bar))
+        : "memory");
 }
 
 // Shared-memory operand of a 16-bit product in 128-byte swizzled blocks of 64
@@ -238,18 +240,20 @@ __host__ __device__ constexpr uint32_t bf16_product(int m, int n, bool a_mn, boo
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 // D (+)= A B for one step of 16 along K; A from shared memory, or from TMEM
-// (two elements a column, the lower in the lower half).
+// (two elements a column, the lower in the lower half). Called by a whole warp
+// with the same arguments, so that operands stay in uniform registers; one
+// lane issues.
 __device__ __forceinline__ void tmem_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "{ .reg .pred p, q; elect.sync _|q, 0xffffffff; setp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
         : "memory");
 }
 __device__ __forceinline__ void tmem_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "{ .reg .pred p, q; elect.sync _|q, 0xffffffff; setp.ne.u32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
         : "memory");
 }

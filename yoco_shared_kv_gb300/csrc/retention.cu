@@ -8,9 +8,9 @@
 //   o_t = scale ( exp(L_t) q_t^T S + sum_(j<=t) exp(L_t - L_j) (q_t . k_j) v_j )
 //   S' = exp(L_C) S + sum_j k_j (exp(L_C - L_j) v_j)^T
 // Every exponent is a difference of running sums with the later one first, so
-// no factor passes 1 for decays of at most 1. The sums run in 64 bits and are
-// kept as two floats: a difference of two neighbours stays exact however far
-// the sum has fallen.
+// no factor passes 1 for decays of at most 1. The sums run as two floats (48
+// bits): a difference of two neighbours stays exact however far the sum has
+// fallen.
 //
 // Kernels.
 //   retention_step: requests of one token. Moves the state once (read and
@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kChunk = 64;         // tokens of a chunk
 constexpr int kSlice = 64;         // value dims of a single token's CTA
-constexpr int kChunkThreads = 256;
+constexpr int kChunkThreads = 256;  // and one warp that issues the products
 constexpr uint64_t kRetWaitNs = 1000000000ull;  // before a wait gives up
 constexpr int kMaxChunks = 512;                 // of a segment
 constexpr int kMaxSegment = kMaxChunks * kChunk;
@@ -71,6 +71,31 @@ struct __align__(16) RetSeg {
 __device__ __forceinline__ float decay_of(const RetParams& p, int64_t token, int32_t h) {
     const float g = __ldg(p.decay + (p.by_token ? token * p.H : 0) + h);
     return g < kMinDecay ? kMinDecay : g;  // a NaN stays one
+}
+
+// A sum as two floats, the second what the first rounds off (48 bits together).
+struct Sum {
+    float h, l;
+};
+__device__ __forceinline__ Sum operator+(Sum a, Sum b) {
+    const float s = a.h + b.h, v = s - a.h;
+    const float e = ((a.h - (s - v)) + (b.h - v)) + (a.l + b.l);
+    const float h = s + e;
+    return {h, e - (h - s)};
+}
+__device__ __forceinline__ float operator-(Sum a, Sum b) { return (a.h - b.h) + (a.l - b.l); }
+__device__ __forceinline__ Sum in_log2(float g) {  // g log2(e)
+    const float h = g * 1.44269502f;                // log2(e) = 1.44269502 + 1.92596e-8
+    return {h, fmaf(g, 1.44269502f, -h) + g * 1.925963033e-8f};
+}
+__device__ __forceinline__ Sum shfl_up(Sum a, int n) {
+    return {__shfl_up_sync(0xffffffffu, a.h, n), __shfl_up_sync(0xffffffffu, a.l, n)};
+}
+__device__ __forceinline__ Sum warp_total(Sum a) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        a = a + Sum{__shfl_xor_sync(0xffffffffu, a.h, off), __shfl_xor_sync(0xffffffffu, a.l, off)};
+    return a;
 }
 
 // Tokens [q0, q1) of request r if it is well formed and has some, else false.
@@ -333,6 +358,7 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
 // end, so that S^T is only ever added to.
 
 constexpr int kVal = 128;        // value dims of a CTA (head_dim 64: half of them idle)
+constexpr int kFactors = 6;      // floats of a token (below)
 constexpr int kBlockBytes = kChunk * 128;  // 64 tokens x 64 elements
 
 template <int D, bool OUT>
@@ -347,14 +373,15 @@ struct RetShape {
     static constexpr int WBUF = OUT || D == 256 ? 1 : 2;       // sets of terms
     static constexpr int STAGES = OUT ? 2 : 3;
     static constexpr int PB = OUT ? kBlockBytes : 0;
-    static constexpr int LB = 8 * (kChunk * 16 + 16);          // sums and factors of 8 chunks
+    static constexpr int FG = OUT ? 4 : 8;                     // chunks whose factors are at hand
+    static constexpr int LB = FG * (kChunk * kFactors * 4 + 8);
     static constexpr int TB = OUT ? 0 : kMaxChunks * 8;        // decay sums of a segment's chunks
     // an operand of 128 rows over a block of 64 reads on into what follows: the
     // last such block is a set of terms at head_dim 64, followed by 8 KiB and more
     static constexpr int PAD = D == 64 ? kBlockBytes : 0;
     static constexpr int SMEM = STAGES * STAGE + WBUF * TERMS + PB + PAD + LB + TB + 1024;
     // tensor memory columns: S^T, its bf16 copy, O1^T, O2^T (and P before it)
-    [[maybe_unused]] static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk, TCOLS = 512;
+    static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk, TCOLS = 512;
     static_assert(!OUT || TO2 + kChunk <= TCOLS, "tensor memory");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -372,7 +399,7 @@ __device__ __forceinline__ uint32_t block_at(int t, int j) {
 }
 
 template <int D, bool OUT>
-__global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetParams p) {
+__global__ void __launch_bounds__(kChunkThreads + 32, 1) retention_chunks(const RetParams p) {
     using S = RetShape<D, OUT>;
     constexpr int NS = S::NS, VD = S::VD;
     extern __shared__ uint8_t ret_smem[];
@@ -382,13 +409,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
     constexpr int AT_W = S::STAGES * S::STAGE, AT_P = AT_W + S::WBUF * S::TERMS, AT_F = AT_P + S::PB + S::PAD;
-    // of each of 8 chunks: sums of 64 tokens (high and low parts, log2 units), exp(L_t) and
-    // exp(L_end - L_t); then exp(L_C)
+    // of each of FG chunks, for its 64 tokens t: the running sum L_t (high and low parts, log2
+    // units), exp(L_t), exp(L_end - L_t), exp(L_t - L_mid), exp(L_mid - L_t); then exp(L_C)
+    // and whether L_mid serves (the chunk's sums span less than 2^100)
     float* const fac = reinterpret_cast<float*>(smem + AT_F);
-    float* const whole = fac + 8 * 4 * kChunk;
-    double* const totals = reinterpret_cast<double*>(smem + AT_F + S::LB);  // !OUT
+    float2* const whole = reinterpret_cast<float2*>(fac + S::FG * kFactors * kChunk);
+    Sum* const totals = reinterpret_cast<Sum*>(smem + AT_F + S::LB);  // !OUT
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int half = warp >> 2;                     // which half of the columns this warp takes
+    const bool issuer = warp == kChunkThreads / 32;  // the warp that issues the products, and nothing else
+    const int half = (warp >> 2) & 1;               // which half of the columns this warp takes
     const int row = (warp & 3) * 32 + lane;         // its lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     if (tid == 0) {
@@ -398,11 +427,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
         mbar_init(&bar_s[1], 1);
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc(&tmem_base, S::TCOLS);
+    if (issuer) tmem_alloc(&tmem_base, S::TCOLS);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tm = tmem_base;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     // single tokens may run beside the segments' pass
     if constexpr (!OUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // phases of the barriers; state updates without outputs, of which two are under way
@@ -421,47 +450,45 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
 
-    for (int32_t item = blockIdx.x; item < items && !bad; item += gridDim.x) {
+    for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const RetSeg sg = p.segs[item / (p.H * NS)];
         const bool last = sg.index == sg.count - 1;
         if (sg.count == 0 || (!OUT && last)) continue;
         const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
 
-        auto load = [&](int32_t c) {  // chunk c into its stage
+        // chunk c into its stage: a thread takes one 16-byte piece of every RS-th row
+        auto load_rows = [&](uint32_t dst, const __nv_bfloat16* src, int64_t stride, int pieces, int32_t left) {
+            const int rs = kChunkThreads / pieces, t0 = tid / pieces, j = tid % pieces;
+            const __nv_bfloat16* at = src + t0 * stride + j * 8;
+            const uint32_t to = dst + block_at(t0, j);  // rs is a multiple of 8: the swizzle stays
+            for (int t = t0; t < kChunk; t += rs) {
+                const bool there = t < left;
+                cp_async_16_or_zero(to + (t - t0) * 128, there ? at : src, there);
+                at += rs * stride;
+            }
+        };
+        auto load = [&](int32_t c) {
+            if (issuer) return;
             const uint32_t st = base + c % S::STAGES * S::STAGE;
             const int32_t left = sg.tokens - c * kChunk;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
-            constexpr int J = D / 8, JV = VD / 8;
-#pragma unroll
-            for (int x = tid; x < kChunk * J; x += kChunkThreads) {
-                const int t = x / J, j = x % J;
-                const bool there = t < left;
-                const int64_t r = there ? t0 + t : t0;
-                if constexpr (OUT)
-                    cp_async_16_or_zero(st + block_at(t, j), p.q + (r * p.H + h) * D + j * 8, there);
-                cp_async_16_or_zero(st + S::QB + block_at(t, j), p.k + (r * H_kv + hk) * D + j * 8, there);
-            }
-#pragma unroll
-            for (int x = tid; x < kChunk * JV; x += kChunkThreads) {
-                const int t = x / JV, j = x % JV;
-                const bool there = t < left;
-                const int64_t r = there ? t0 + t : t0;
-                cp_async_16_or_zero(st + S::QB + S::KB + block_at(t, j), p.v + (r * H_kv + hk) * D + dv0 + j * 8, there);
-            }
+            if constexpr (OUT)
+                load_rows(st, p.q + (t0 * p.H + h) * D, static_cast<int64_t>(p.H) * D, D / 8, left);
+            load_rows(st + S::QB, p.k + (t0 * H_kv + hk) * D, static_cast<int64_t>(H_kv) * D, D / 8, left);
+            load_rows(st + S::QB + S::KB, p.v + (t0 * H_kv + hk) * D + dv0, static_cast<int64_t>(H_kv) * D, VD / 8, left);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         __syncthreads();  // the previous item is done with shared and tensor memory
         load(0);
         if (S::STAGES == 3 && chunks > 1) load(1);
 
-        // log decays of chunk cc (log2 units): lane l has tokens 2l and 2l + 1
-        auto decays = [&](int32_t cc, double& g0, double& g1) {
+        // log decays of chunk cc: lane l has tokens 2l and 2l + 1
+        auto decays = [&](int32_t cc, Sum& g0, Sum& g1) {
             const int64_t t0 = sg.token + static_cast<int64_t>(cc) * kChunk;
             const int32_t left = cc < chunks ? min(kChunk, sg.tokens - cc * kChunk) : 0;
-            constexpr double kLog2E = 1.4426950408889634074;
-            g0 = 2 * lane < left ? kLog2E * static_cast<double>(decay_of(p, t0 + 2 * lane, h)) : 0.0;
-            g1 = 2 * lane + 1 < left ? kLog2E * static_cast<double>(decay_of(p, t0 + 2 * lane + 1, h)) : 0.0;
+            g0 = 2 * lane < left ? in_log2(decay_of(p, t0 + 2 * lane, h)) : Sum{0.f, 0.f};
+            g1 = 2 * lane + 1 < left ? in_log2(decay_of(p, t0 + 2 * lane + 1, h)) : Sum{0.f, 0.f};
         };
         if constexpr (OUT) {  // the state before the segment
             const float* src = nullptr;
@@ -471,69 +498,75 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
             else if (__ldg(p.seq_lens + sg.req) > q)
                 src = p.state + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
             if (row >= VD) src = nullptr;
+            if (!issuer) {
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                const int c0 = half * (D / 2) + b * 32;
-                uint32_t x[32];
+                for (int b = 0; b < D / 64; ++b) {
+                    const int c0 = half * (D / 2) + b * 32;
+                    uint32_t x[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    x[i] = src ? __float_as_uint(src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
-                tmem_st32(tm + lanes + S::TS + c0, x);
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = src ? __float_as_uint(src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
+                    tmem_st32(tm + lanes + S::TS + c0, x);
+                }
+                tmem_st_wait();
             }
-            tmem_st_wait();
         } else {  // decay sums of the segment's chunks
-            for (int32_t cc = warp; cc < chunks; cc += 8) {
-                double g0, g1;
-                decays(cc, g0, g1);
-                double t = g0 + g1;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-                if (lane == 0) totals[cc] = t;
-            }
+            if (!issuer)
+                for (int32_t cc = warp; cc < chunks; cc += 8) {
+                    Sum g0, g1;
+                    decays(cc, g0, g1);
+                    const Sum t = warp_total(g0 + g1);
+                    if (lane == 0) totals[cc] = t;
+                }
             __syncthreads();
         }
         bool pending = false;  // an update of the state is under way
 
         for (int32_t c = 0; c < chunks; ++c) {
-            if ((c & 7) == 0) {  // running sums and factors of 8 chunks, one a warp
+            if (c % S::FG == 0) {  // running sums and factors of the next chunks, one a warp
                 if (c) __syncthreads();
-                const int32_t cc = c + warp;
-                double g0, g1;
-                decays(cc, g0, g1);
-                double sum = g0 + g1;
+                if (warp < S::FG) {
+                    const int32_t cc = c + warp;
+                    Sum g0, g1;
+                    decays(cc, g0, g1);
+                    Sum l1 = g0 + g1;
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const double x = __shfl_up_sync(0xffffffffu, sum, off);
-                    if (lane >= off) sum += x;
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const Sum x = shfl_up(l1, off);
+                        if (lane >= off) l1 = l1 + x;
+                    }
+                    const Sum l0 = l1 + Sum{-g1.h, -g1.l};
+                    auto of_lane = [](Sum a, int l) {
+                        return Sum{__shfl_sync(0xffffffffu, a.h, l), __shfl_sync(0xffffffffu, a.l, l)};
+                    };
+                    const Sum total = of_lane(l1, 31);
+                    Sum end = total;
+                    if constexpr (!OUT) {  // to the end of the segment
+                        Sum t = {0.f, 0.f};
+                        for (int32_t x = cc + 1 + lane; x < chunks; x += 32) t = t + totals[x];
+                        end = end + warp_total(t);
+                    }
+                    auto put = [&](int i, float x, float y) {
+                        *reinterpret_cast<float2*>(fac + (warp * kFactors + i) * kChunk + 2 * lane) = make_float2(x, y);
+                    };
+                    put(3, exp2f(end - l0), exp2f(end - l1));
+                    if constexpr (OUT) {
+                        const Sum first = of_lane(l0, 0), mid = of_lane(l0, 16);
+                        put(0, l0.h, l1.h);
+                        put(1, l0.l, l1.l);
+                        put(2, exp2f(l0.h), exp2f(l1.h));
+                        put(4, exp2f(l0 - mid), exp2f(l1 - mid));
+                        put(5, exp2f(mid - l0), exp2f(mid - l1));
+                        if (lane == 0) whole[warp] = make_float2(exp2f(total.h), fabsf(first - total) < 100.f ? 1.f : 0.f);
+                    }
                 }
-                const double total = __shfl_sync(0xffffffffu, sum, 31);
-                double end = total;
-                if constexpr (!OUT) {  // to the end of the segment
-                    double t = 0.0;
-                    for (int32_t x = cc + 1 + lane; x < chunks; x += 32) t += totals[x];
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-                    end += t;
-                }
-                auto put = [&](int i, float x, float y) {
-                    *reinterpret_cast<float2*>(fac + (warp * 4 + i) * kChunk + 2 * lane) = make_float2(x, y);
-                };
-                const double l0 = sum - g1, l1 = sum;
-                const float h0 = static_cast<float>(l0), h1 = static_cast<float>(l1);
-                if constexpr (OUT) {
-                    put(0, h0, h1);
-                    put(1, static_cast<float>(l0 - h0), static_cast<float>(l1 - h1));
-                    put(2, exp2f(h0), exp2f(h1));
-                }
-                put(3, exp2f(static_cast<float>(end - l0)), exp2f(static_cast<float>(end - l1)));
-                if (lane == 0) whole[warp] = exp2f(static_cast<float>(total));
             }
             const uint32_t at = c % S::STAGES * S::STAGE;  // of the chunk's q, k, v
             const uint32_t sq = base + at, sk = sq + S::QB, sv = sk + S::KB;
             const uint32_t aw = AT_W + (S::WBUF == 2 ? (c & 1) * S::TERMS : 0);
-            const float* f = fac + (c & 7) * 4 * kChunk;
+            const float* f = fac + c % S::FG * kFactors * kChunk;
             const bool update = !OUT || last || c + 1 < chunks;
-            const int terms = (!OUT || last) ? 3 : 2;
+            const bool three = !OUT || last;  // terms of the decayed v
 
             if (S::STAGES == 3 && c + 1 < chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
             else asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -545,9 +578,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
             if (bad) break;
             tmem_fence_after();
             if (!OUT && S::WBUF == 1 && c + 2 < chunks) load(c + 2);
-            if constexpr (OUT) {
-                if (c + 1 < chunks) load(c + 1);
-                if (tid == 0) {  // P = q k^T (128 rows: the upper 64 are not looked at)
+            if (OUT && c + 1 < chunks) load(c + 1);
+            if (issuer) {
+                if constexpr (OUT) {  // P = q k^T (128 rows: the upper 64 are not looked at)
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t o = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
@@ -556,100 +589,106 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                     }
                     tmem_commit(&bar_p);
                 }
-                __syncwarp();
-                // the state as a bf16 operand, then scaled by the chunk's decay
-                const float aC = whole[c & 7];
+            } else {
+                if (update) {  // exp(L_end - L_j) v_j in bf16 terms, each cut from what the ones before leave
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b) {
-                    const int c0 = half * (D / 2) + b * 32;
-                    uint32_t x[32], y[16];
-                    tmem_ld32(tm + lanes + S::TS + c0, x);
-                    tmem_ld_wait();
+                    for (int x = tid; x < kChunk * (VD / 8); x += kChunkThreads) {
+                        const int t = x / (VD / 8), j = x % (VD / 8);
+                        const uint32_t o = block_at(t, j);
+                        const uint4 w = *reinterpret_cast<const uint4*>(smem + at + S::QB + S::KB + o);
+                        const float fw = f[3 * kChunk + t];
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t r[3][4];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        y[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                        x[2 * i] = __float_as_uint(__uint_as_float(x[2 * i]) * aC);
-                        x[2 * i + 1] = __float_as_uint(__uint_as_float(x[2 * i + 1]) * aC);
-                    }
-                    tmem_st16(tm + lanes + S::TC + c0 / 2, y);
-                    if (update) tmem_st32(tm + lanes + S::TS + c0, x);
-                }
-            }
-            if (update) {  // exp(L_end - L_j) v_j in bf16 terms
+                        for (int i = 0; i < 4; ++i) {
+                            float lo = bf16lo_to_f32(in[i]) * fw, hi = bf16hi_to_f32(in[i]) * fw;
 #pragma unroll
-                for (int x = tid; x < kChunk * (VD / 8); x += kChunkThreads) {
-                    const int t = x / (VD / 8), j = x % (VD / 8);
-                    const uint32_t o = block_at(t, j);
-                    const uint4 w = *reinterpret_cast<const uint4*>(smem + at + S::QB + S::KB + o);
-                    const float fw = f[3 * kChunk + t];
-                    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t r[3][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo = bf16lo_to_f32(in[i]) * fw, hi = bf16hi_to_f32(in[i]) * fw;
-#pragma unroll
-                        for (int u = 0; u < 3; ++u) {
-                            r[u][i] = pack_bf16x2(lo, hi);
-                            lo -= bf16lo_to_f32(r[u][i]);
-                            hi -= bf16hi_to_f32(r[u][i]);
+                            for (int u = 0; u < 3; ++u) {
+                                r[u][i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+                                lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+                                hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int u = 0; u < 3; ++u)
-                        *reinterpret_cast<uint4*>(smem + aw + u * S::VB + o) =
-                            make_uint4(r[u][0], r[u][1], r[u][2], r[u][3]);
+                        for (int u = 0; u < 3; ++u)
+                            if (u < 2 || three)
+                                *reinterpret_cast<uint4*>(smem + aw + u * S::VB + o) =
+                                    make_uint4(r[u][0], r[u][1], r[u][2], r[u][3]);
+                    }
+                }
+                if constexpr (OUT) {  // the state as a bf16 operand, then scaled by the chunk's decay
+                    const float aC = whole[c % S::FG].x;
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b) {
+                        const int c0 = half * (D / 2) + b * 32;
+                        uint32_t x[32], y[16];
+                        tmem_ld32(tm + lanes + S::TS + c0, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            y[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                            x[2 * i] = __float_as_uint(__uint_as_float(x[2 * i]) * aC);
+                            x[2 * i + 1] = __float_as_uint(__uint_as_float(x[2 * i + 1]) * aC);
+                        }
+                        tmem_st16(tm + lanes + S::TC + c0 / 2, y);
+                        if (update) tmem_st32(tm + lanes + S::TS + c0, x);
+                    }
+                    tmem_st_wait();
                 }
             }
             fence_proxy_async_smem();
-            if constexpr (OUT) tmem_st_wait();
             tmem_fence_before();
             __syncthreads();  // the state's copy and the terms are complete
+            tmem_fence_after();
             if constexpr (OUT) {
-                if (tid == 0) {  // O1^T = S^T q^T
-                    tmem_fence_after();
+                if (issuer) {  // O1^T = S^T q^T
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         tmem_mma_ta(tm + S::TO1, tm + S::TC + kk * 8,
                                     smem_operand(sq + (kk >> 2) * kBlockBytes + (kk & 3) * 32, 16, 1024),
                                     bf16_product(128, kChunk, false, false), kk > 0);
-                }
-                __syncwarp();
-                wait(&bar_p, ph_p);
-                tmem_fence_after();
-                if (row < kChunk) {  // warps 0, 1, 4, 5: weights of token `row`, 32 earlier tokens
-                    uint32_t x[32];
-                    tmem_ld32(tm + lanes + S::TO2 + half * 32, x);
-                    tmem_ld_wait();
-                    const float th = f[row], tl = f[kChunk + row];
+                    ph_p ^= 1;
+                } else {
+                    wait(&bar_p, ph_p);
+                    tmem_fence_after();
+                    if (row < kChunk) {  // warps 0, 1, 4, 5: weights of token `row`, 32 earlier tokens
+                        uint32_t x[32];
+                        tmem_ld32(tm + lanes + S::TO2 + half * 32, x);
+                        tmem_ld_wait();
+                        const bool near = whole[c % S::FG].y != 0.f;
+                        const float th = f[row], tl = f[kChunk + row], tm_ = f[4 * kChunk + row];
 #pragma unroll
-                    for (int q8 = 0; q8 < 4; ++q8) {
-                        const int j0 = half * 32 + q8 * 8;
-                        uint32_t w[4];
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const float4 jh = *reinterpret_cast<const float4*>(f + j0 + 4 * v);
-                            const float4 jl = *reinterpret_cast<const float4*>(f + kChunk + j0 + 4 * v);
-                            const float d[4] = {(th - jh.x) + (tl - jl.x), (th - jh.y) + (tl - jl.y),
-                                                (th - jh.z) + (tl - jl.z), (th - jh.w) + (tl - jl.w)};
-                            float y[4];
+                        for (int q4 = 0; q4 < 8; ++q4) {
+                            const int j0 = half * 32 + q4 * 4;
+                            float w[4];
+                            if (near) {  // one factor of the row, one of the column
+                                const float4 m = *reinterpret_cast<const float4*>(f + 5 * kChunk + j0);
+                                w[0] = tm_ * m.x;
+                                w[1] = tm_ * m.y;
+                                w[2] = tm_ * m.z;
+                                w[3] = tm_ * m.w;
+                            } else {
+                                const float4 jh = *reinterpret_cast<const float4*>(f + j0);
+                                const float4 jl = *reinterpret_cast<const float4*>(f + kChunk + j0);
+                                w[0] = exp2_approx((th - jh.x) + (tl - jl.x));
+                                w[1] = exp2_approx((th - jh.y) + (tl - jl.y));
+                                w[2] = exp2_approx((th - jh.z) + (tl - jl.z));
+                                w[3] = exp2_approx((th - jh.w) + (tl - jl.w));
+                            }
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                y[i] = j0 + 4 * v + i <= row
-                                           ? __uint_as_float(x[q8 * 8 + 4 * v + i]) * exp2_approx(d[i])
-                                           : 0.f;
-                            w[2 * v] = pack_bf16x2(y[0], y[1]);
-                            w[2 * v + 1] = pack_bf16x2(y[2], y[3]);
+                                w[i] = j0 + i <= row ? w[i] * __uint_as_float(x[q4 * 4 + i]) : 0.f;
+                            *reinterpret_cast<uint2*>(smem + AT_P + block_at(row, half * 4 + (q4 >> 1)) + (q4 & 1) * 8) =
+                                make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
                         }
-                        *reinterpret_cast<uint4*>(smem + AT_P + block_at(row, half * 4 + q8)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 fence_proxy_async_smem();
                 tmem_fence_before();
                 __syncthreads();  // P is in shared memory, its columns are free
-            }
-            if (tid == 0) {
                 tmem_fence_after();
+            }
+            if (issuer) {
                 if constexpr (OUT) {  // O2^T = v^T P^T
 #pragma unroll
                     for (int kk = 0; kk < kChunk / 16; ++kk)
@@ -657,42 +696,51 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                                  smem_operand(base + AT_P + kk * 32, 16, 1024), bf16_product(128, kChunk, true, false),
                                  kk > 0);
                     tmem_commit(&bar_o);
+                    ph_o ^= 1;
                 }
                 if (update) {  // S^T += (decayed v)^T k
-                    for (int u = 0; u < terms; ++u)
 #pragma unroll
-                        for (int kk = 0; kk < kChunk / 16; ++kk)
-                            tmem_mma(tm + S::TS, smem_operand(base + aw + u * S::VB + kk * 2048, kBlockBytes, 1024),
-                                     smem_operand(sk + kk * 2048, kBlockBytes, 1024), bf16_product(128, D, true, true),
-                                     OUT || c > 0 || u > 0 || kk > 0);
+                    for (int u = 0; u < 3; ++u)
+                        if (u < 2 || three)
+#pragma unroll
+                            for (int kk = 0; kk < kChunk / 16; ++kk)
+                                tmem_mma(tm + S::TS, smem_operand(base + aw + u * S::VB + kk * 2048, kBlockBytes, 1024),
+                                         smem_operand(sk + kk * 2048, kBlockBytes, 1024),
+                                         bf16_product(128, D, true, true), OUT || c > 0 || u > 0 || kk > 0);
                     tmem_commit(&bar_s[OUT ? 0 : c & 1]);
                 }
             }
-            __syncwarp();
             if constexpr (OUT) {
                 pending = update;
-                wait(&bar_o, ph_o);
-                tmem_fence_after();
-                uint32_t a[32], b[32];
-                tmem_ld32(tm + lanes + S::TO1 + half * 32, a);
-                tmem_ld32(tm + lanes + S::TO2 + half * 32, b);
-                tmem_ld_wait();
-                const int32_t left = sg.tokens - c * kChunk - half * 32;
-                // Two lanes exchange, so that each writes two value dims of every other token: a
-                // warp's 32 lanes are 64 bytes of two tokens' rows.
-                const bool odd = lane & 1;
-                uint32_t* dst = reinterpret_cast<uint32_t*>(
-                    p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + half * 32 + odd) * p.H + h) * D + dv0 +
-                    (row & ~1));
-                const float* et = f + 2 * kChunk + half * 32;
+                if (!issuer) {
+                    wait(&bar_o, ph_o);
+                    tmem_fence_after();
+                    uint32_t a[32], b[32];
+                    tmem_ld32(tm + lanes + S::TO1 + half * 32, a);
+                    tmem_ld32(tm + lanes + S::TO2 + half * 32, b);
+                    tmem_ld_wait();
+                    // to rows of tokens, in the place of the chunk's q, whose products are done
+                    const float* et = f + 2 * kChunk + half * 32;
+                    uint8_t* to = smem + at + half * 32 * (2 * VD) + 2 * row;
+                    if (row < VD) {
 #pragma unroll
-                for (int t = 0; t < 32; t += 2) {
-                    const float2 e2 = *reinterpret_cast<const float2*>(et + t);
-                    const float y0 = p.scale * fmaf(e2.x, __uint_as_float(a[t]), __uint_as_float(b[t]));
-                    const float y1 = p.scale * fmaf(e2.y, __uint_as_float(a[t + 1]), __uint_as_float(b[t + 1]));
-                    const float z = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-                    if (row < VD && t + odd < left)
-                        dst[static_cast<int64_t>(t) * p.H * (D / 2)] = odd ? pack_bf16x2(z, y1) : pack_bf16x2(y0, z);
+                        for (int t = 0; t < 32; ++t)
+                            *reinterpret_cast<__nv_bfloat16*>(to + t * (2 * VD)) = __float2bfloat16_rn(
+                                p.scale * fmaf(et[t], __uint_as_float(a[t]), __uint_as_float(b[t])));
+                    }
+                    asm volatile("bar.sync 1, %0;" ::"n"(kChunkThreads) : "memory");  // all but the issuer
+                    const int32_t left = sg.tokens - c * kChunk;
+                    constexpr int J = VD / 8, RS = kChunkThreads / J;
+                    const int t0 = tid / J, j = tid % J;
+                    const uint8_t* from = smem + at + t0 * (2 * VD) + j * 16;
+                    __nv_bfloat16* dst =
+                        p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + t0) * p.H + h) * D + dv0 + j * 8;
+#pragma unroll
+                    for (int t = 0; t < kChunk; t += RS) {
+                        if (t0 + t < left)
+                            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(from + t * (2 * VD));
+                        dst += static_cast<int64_t>(RS) * p.H * D;
+                    }
                 }
             } else {
                 // the products of the chunk before are done with its stage and terms
@@ -701,7 +749,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
                 if (S::WBUF == 2 && c + 2 < chunks) load(c + 2);
             }
         }
-        if (pending) wait_update(chunks - 1);
+        if (!bad && pending) wait_update(chunks - 1);
         bad = __syncthreads_or(bad);
         if (bad) break;
         tmem_fence_after();
@@ -711,7 +759,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
             dst = p.slots + (static_cast<int64_t>(sg.slot + 1) * p.H + h) * D * D + dv0;
         else if (last)
             dst = p.state_out + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
-        if (dst) {
+        if (dst && !issuer) {
 #pragma unroll
             for (int b = 0; b < D / 64; ++b) {
                 const int c0 = half * (D / 2) + b * 32;
@@ -724,11 +772,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
             }
         }
         if (!OUT && dv0 == 0 && warp == 0) {  // the segment's decay
-            double t = 0.0;
-            for (int32_t x = lane; x < chunks; x += 32) t += totals[x];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-            if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(static_cast<float>(t));
+            Sum t = {0.f, 0.f};
+            for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
+            t = warp_total(t);
+            if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(t.h);
         }
         tmem_fence_before();
     }
@@ -737,7 +784,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) retention_chunks(const RetPa
     __syncthreads();
     tmem_fence_after();
     if (bad && tid == 0) set_err(p.err, YOCO_DEVERR_TIMEOUT);
-    if (warp == 0) tmem_dealloc(tm, S::TCOLS);
+    if (issuer) tmem_dealloc(tm, S::TCOLS);
 }
 
 // ------------------------------------------------------------------ host side
@@ -818,7 +865,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);  // one CTA an SM
     retention_plan<<<1, 1024, 0, s>>>(p, units, sms);
     if (cut) {
-        retention_chunks<D, false><<<grid, kChunkThreads, RetShape<D, false>::SMEM, s>>>(p);
+        retention_chunks<D, false><<<grid, kChunkThreads + 32, RetShape<D, false>::SMEM, s>>>(p);
         // single tokens: bound by HBM, they run beside the segments' products
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -834,7 +881,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
         const int64_t parts = static_cast<int64_t>(p.max_segs) * p.H * (D * D / 1024);
         retention_scan<D><<<static_cast<unsigned>(parts < 16 * sms ? parts : 16 * sms), 256, 0, s>>>(p);
     }
-    retention_chunks<D, true><<<grid, kChunkThreads, RetShape<D, true>::SMEM, s>>>(p);
+    retention_chunks<D, true><<<grid, kChunkThreads + 32, RetShape<D, true>::SMEM, s>>>(p);
     return cudaGetLastError();
 }
 
