@@ -16,11 +16,11 @@
 //   retention_step: requests of one token. Moves the state once (read and
 //     write, fp32): bound by HBM.
 //   retention_plan: cuts the longer requests into segments of whole chunks.
-//   retention_chunks<.., false>: the state that each segment but a request's
+//   retention_add: the state that each segment but a request's
 //     last adds (from zero), all segments at once.
 //   retention_scan: runs along a request's segments and turns those into the
 //     state before each segment.
-//   retention_chunks<.., true>: outputs of every segment, chunk by chunk, and
+//   retention_out: outputs of every segment, chunk by chunk, and
 //     the state after a request's last one.
 // A request of one segment needs neither the second pass nor the scan.
 #include "common.cuh"
@@ -30,7 +30,8 @@ namespace {
 
 constexpr int kChunk = 64;         // tokens of a chunk
 constexpr int kSlice = 64;         // value dims of a single token's CTA
-constexpr int kChunkThreads = 256;  // and one warp that issues the products
+constexpr int kAddThreads = 256;   // and one warp that issues the products
+constexpr int kOutThreads = 512;   // likewise
 constexpr uint64_t kRetWaitNs = 1000000000ull;  // before a wait gives up
 constexpr int kMaxChunks = 512;                 // of a segment
 constexpr int kMaxSegment = kMaxChunks * kChunk;
@@ -210,6 +211,7 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
     __shared__ int32_t tot[2][32];
     __shared__ int64_t cost[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (p.max_slots > 0 && p.num_reqs <= kChooseReqs) {
         const float grown = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(warp) / 6.f);
         const int32_t seg = min((static_cast<int32_t>(fminf(grown, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
@@ -298,6 +300,7 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
 template <int D>
 __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
     constexpr int PARTS = D * D / 1024;  // CTAs of a (request, head)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t n = *p.num_segs;
     for (int64_t item = blockIdx.x; item < static_cast<int64_t>(n) * p.H * PARTS; item += gridDim.x) {
         const RetSeg s = p.segs[item / (p.H * PARTS)];
@@ -345,45 +348,27 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
 // the full 128 x 256 shape):
 //   P (tokens x tokens)  = q k^T
 //   O1^T (value x token) = S^T q^T            S^T as a bf16 copy in tensor memory
-//   O2^T                 = v^T P^T            P decayed, bf16, in shared memory
 //   S^T                 += (decayed v)^T k    after S^T was scaled by exp(L_C)
+//   O2^T                 = v^T P^T            P decayed, bf16, in shared memory
 // q, k and v lie in shared memory as blocks of 64 elements a row with the
 // 128-byte swizzle, which serve as K-major and as MN-major operands alike: no
 // operand is transposed by a thread. Roundings to bf16: P and the state's copy,
 // both below the rounding of the output; the decayed v as a sum of three bf16
 // terms (24 bits) where the state leaves the kernel, of two (16 bits) where it
 // only feeds later outputs of its segment.
-//
-// Without outputs (the states that segments add) v is decayed to the segment's
-// end, so that S^T is only ever added to.
 
-constexpr int kVal = 128;        // value dims of a CTA (head_dim 64: half of them idle)
-constexpr int kFactors = 6;      // floats of a token (below)
+constexpr int kVal = 128;                  // value dims of a CTA (head_dim 64: 64 of its rows idle)
 constexpr int kBlockBytes = kChunk * 128;  // 64 tokens x 64 elements
+constexpr int kTensorCols = 512;
 
-template <int D, bool OUT>
-struct RetShape {
-    static constexpr int VD = D < kVal ? D : kVal;             // value dims a CTA really has
-    static constexpr int NS = D / VD;                          // slices of a head
-    static constexpr int QB = OUT ? D / 64 * kBlockBytes : 0;
-    static constexpr int KB = D / 64 * kBlockBytes;
-    static constexpr int VB = VD / 64 * kBlockBytes;
-    static constexpr int STAGE = QB + KB + VB;
-    static constexpr int TERMS = 3 * VB;                       // decayed v, three terms
-    static constexpr int WBUF = OUT || D == 256 ? 1 : 2;       // sets of terms
-    static constexpr int STAGES = OUT ? 2 : 3;
-    static constexpr int PB = OUT ? kBlockBytes : 0;
-    static constexpr int FG = OUT ? 4 : 8;                     // chunks whose factors are at hand
-    static constexpr int LB = FG * (kChunk * kFactors * 4 + 8);
-    static constexpr int TB = OUT ? 0 : kMaxChunks * 8;        // decay sums of a segment's chunks
-    // an operand of 128 rows over a block of 64 reads on into what follows: the
-    // last such block is a set of terms at head_dim 64, followed by 8 KiB and more
+// Value dims a CTA really has, slices of a head, bytes of a chunk's q or k and v.
+template <int D>
+struct RetDims {
+    static constexpr int VD = D < kVal ? D : kVal, NS = D / VD;
+    static constexpr int KB = D / 64 * kBlockBytes, VB = VD / 64 * kBlockBytes;
+    // an operand of 128 rows over a block of 64 reads on into what follows; at head_dim 64
+    // that can be the end of the terms
     static constexpr int PAD = D == 64 ? kBlockBytes : 0;
-    static constexpr int SMEM = STAGES * STAGE + WBUF * TERMS + PB + PAD + LB + TB + 1024;
-    // tensor memory columns: S^T, its bf16 copy, O1^T, O2^T (and P before it)
-    static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk, TCOLS = 512;
-    static_assert(!OUT || TO2 + kChunk <= TCOLS, "tensor memory");
-    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 // 16 bytes global -> shared, or zeros.
@@ -392,105 +377,368 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* sr
                  "l"(reinterpret_cast<uint64_t>(src)), "r"(there ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Byte offset of 16-byte piece j of row t in swizzled blocks of 8 pieces a row.
 __device__ __forceinline__ uint32_t block_at(int t, int j) {
     return static_cast<uint32_t>((j >> 3) * kBlockBytes + t * 128 + (((j & 7) ^ (t & 7)) << 4));
 }
 
-template <int D, bool OUT>
-__global__ void __launch_bounds__(kChunkThreads + 32, 1) retention_chunks(const RetParams p) {
-    using S = RetShape<D, OUT>;
-    constexpr int NS = S::NS, VD = S::VD;
+// Rows of a chunk (PIECES 16-byte pieces each, `left` of them there, zeros behind) into
+// swizzled blocks, by THREADS threads: each takes one piece of every few rows.
+template <int PIECES, int THREADS>
+__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* src, int64_t stride, int32_t left,
+                                          int thread) {
+    constexpr int RS = THREADS / PIECES;  // rows a pass takes
+    static_assert(RS >= 4 && (RS == 4 || RS % 8 == 0), "the swizzle of a thread's rows");
+    const int t0 = thread / PIECES, j = thread % PIECES;
+    const __nv_bfloat16* at = src + t0 * stride + j * 8;
+#pragma unroll
+    for (int t = 0; t < kChunk; t += RS) {
+        const bool there = t0 + t < left;
+        cp_async_16_or_zero(dst + block_at(t0 + t, j), there ? at : src, there);
+        at += RS * stride;
+    }
+}
+
+// exp(L_end - L_j) v_j as bf16 terms, each cut from what the ones before it leave, into
+// `terms` (VB bytes each); w: the factors of the chunk's tokens.
+template <int VD, int VB, int THREADS>
+__device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, const float* w, bool three, int thread) {
+#pragma unroll
+    for (int x = thread; x < kChunk * (VD / 8); x += THREADS) {
+        const int t = x / (VD / 8), j = x % (VD / 8);
+        const uint32_t o = block_at(t, j);
+        const uint4 in4 = *reinterpret_cast<const uint4*>(v + o);
+        const float fw = w[t];
+        const uint32_t in[4] = {in4.x, in4.y, in4.z, in4.w};
+        uint32_t r0[4], r1[4], r2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo = bf16lo_to_f32(in[i]) * fw, hi = bf16hi_to_f32(in[i]) * fw;
+            r0[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+            hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
+            r1[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            if (three) {
+                lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+                hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
+                r2[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+            }
+        }
+        *reinterpret_cast<uint4*>(terms + o) = make_uint4(r0[0], r0[1], r0[2], r0[3]);
+        *reinterpret_cast<uint4*>(terms + VB + o) = make_uint4(r1[0], r1[1], r1[2], r1[3]);
+        if (three) *reinterpret_cast<uint4*>(terms + 2 * VB + o) = make_uint4(r2[0], r2[1], r2[2], r2[3]);
+    }
+}
+
+// S^T += (decayed v)^T k; the issuing warp.
+template <int D>
+__device__ __forceinline__ void issue_update(uint32_t state, uint32_t terms, uint32_t k, bool three, bool add) {
+    constexpr uint32_t ID = bf16_product(128, D, true, true);
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+        if (u < 2 || three)
+#pragma unroll
+            for (int kk = 0; kk < kChunk / 16; ++kk)
+                tmem_mma(state, smem_operand(terms + u * RetDims<D>::VB + kk * 2048, kBlockBytes, 1024),
+                         smem_operand(k + kk * 2048, kBlockBytes, 1024), ID, add || u > 0 || kk > 0);
+}
+
+// Log decays of chunk c of a segment: lane l has tokens 2l and 2l + 1 (0 behind the last).
+__device__ __forceinline__ float2 chunk_decays(const RetParams& p, const RetSeg& sg, int32_t h, int32_t c, int lane) {
+    const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
+    const int32_t left = sg.tokens - c * kChunk;
+    return make_float2(2 * lane < left ? decay_of(p, t0 + 2 * lane, h) : 0.f,
+                       2 * lane + 1 < left ? decay_of(p, t0 + 2 * lane + 1, h) : 0.f);
+}
+// Running sums over the chunk, up to and with tokens 2l and 2l + 1.
+__device__ __forceinline__ void running_sums(float2 g, int lane, Sum& l0, Sum& l1) {
+    const Sum g1 = in_log2(g.y);
+    l1 = in_log2(g.x) + g1;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Sum x = shfl_up(l1, off);
+        if (lane >= off) l1 = l1 + x;
+    }
+    l0 = l1 + Sum{-g1.h, -g1.l};
+}
+
+// What segments add. v is decayed to the segment's end, so that S^T is only ever added to.
+// Copies run ahead (k of the next chunk, v of the one after), products behind: the terms of
+// a chunk are worked out while the products of the one before run.
+template <int D>
+struct RetAddShape : RetDims<D> {
+    using B = RetDims<D>;
+    static constexpr int AT_V = 2 * B::KB, AT_W = AT_V + 3 * B::VB, AT_F = AT_W + 2 * 3 * B::VB + B::PAD;
+    static constexpr int AT_T = AT_F + 2 * kChunk * 4;  // factors of two chunks, then decay sums of all
+    static constexpr int SMEM = AT_T + kMaxChunks * 8 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetParams p) {
+    using S = RetAddShape<D>;
+    constexpr int NS = S::NS, VD = S::VD, T = kAddThreads;
     extern __shared__ uint8_t ret_smem[];
-    __shared__ __align__(8) uint64_t bar_p, bar_o, bar_s[2];
+    __shared__ __align__(8) uint64_t bars[2];  // the products of even and odd chunks
     __shared__ uint32_t tmem_base;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ret_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
-    constexpr int AT_W = S::STAGES * S::STAGE, AT_P = AT_W + S::WBUF * S::TERMS, AT_F = AT_P + S::PB + S::PAD;
-    // of each of FG chunks, for its 64 tokens t: the running sum L_t (high and low parts, log2
-    // units), exp(L_t), exp(L_end - L_t), exp(L_t - L_mid), exp(L_mid - L_t); then exp(L_C)
-    // and whether L_mid serves (the chunk's sums span less than 2^100)
-    float* const fac = reinterpret_cast<float*>(smem + AT_F);
-    float2* const whole = reinterpret_cast<float2*>(fac + S::FG * kFactors * kChunk);
-    Sum* const totals = reinterpret_cast<Sum*>(smem + AT_F + S::LB);  // !OUT
+    float* const fac = reinterpret_cast<float*>(smem + S::AT_F);
+    Sum* const totals = reinterpret_cast<Sum*>(smem + S::AT_T);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool issuer = warp == kChunkThreads / 32;  // the warp that issues the products, and nothing else
-    const int half = (warp >> 2) & 1;               // which half of the columns this warp takes
-    const int row = (warp & 3) * 32 + lane;         // its lane of tensor memory
+    const bool issuer = warp == T / 32;  // the warp that issues the products
+    const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     if (tid == 0) {
-        mbar_init(&bar_p, 1);
-        mbar_init(&bar_o, 1);
-        mbar_init(&bar_s[0], 1);
-        mbar_init(&bar_s[1], 1);
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
         fence_mbar_init();
     }
-    if (issuer) tmem_alloc(&tmem_base, S::TCOLS);
+    if (issuer) tmem_alloc(&tmem_base, kTensorCols);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
-    // single tokens may run beside the segments' pass
-    if constexpr (!OUT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // phases of the barriers; state updates without outputs, of which two are under way
-    // at once, take the two of bar_s in turn
-    uint32_t ph_p = 0, ph_o = 0, ph_s[2] = {0, 0};
-    bool bad = false;                       // a wait has given up
+    asm volatile("griddepcontrol.wait;" ::: "memory");               // the segments are listed
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // single tokens may run beside this
+    uint32_t ph[2] = {0, 0};
+    bool bad = false;  // a wait has given up
+    auto wait = [&](int32_t c) {
+        const int i = c & 1;
+        if (!bad && !mbar_wait_bounded(&bars[i], i ? ph[1] : ph[0], kRetWaitNs)) bad = true;
+        if (i) ph[1] ^= 1;
+        else ph[0] ^= 1;
+    };
+    const int32_t H_kv = p.H / p.G;
+    const int32_t items = *p.num_segs * p.H * NS;
+    for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const RetSeg sg = p.segs[item / (p.H * NS)];
+        if (sg.count == 0 || sg.index == sg.count - 1) continue;
+        const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
+        const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
+        auto load_k = [&](int32_t c) {
+            if (issuer || c >= chunks) return;
+            const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
+            load_rows<D / 8, T>(base + (c & 1) * S::KB, p.k + (t0 * H_kv + hk) * D, static_cast<int64_t>(H_kv) * D,
+                                sg.tokens - c * kChunk, tid);
+        };
+        auto load_v = [&](int32_t c) {
+            if (issuer || c >= chunks) return;
+            const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
+            load_rows<VD / 8, T>(base + S::AT_V + c % 3 * S::VB, p.v + (t0 * H_kv + hk) * D + dv0,
+                                 static_cast<int64_t>(H_kv) * D, sg.tokens - c * kChunk, tid);
+        };
+        // factors of chunk c from its decays: one warp
+        auto factors = [&](int32_t c, float2 g) {
+            Sum l0, l1;
+            running_sums(g, lane, l0, l1);
+            Sum end = {0.f, 0.f};  // of this chunk and all after it
+            for (int32_t x = c + lane; x < chunks; x += 32) end = end + totals[x];
+            end = warp_total(end);
+            *reinterpret_cast<float2*>(fac + (c & 1) * kChunk + 2 * lane) = make_float2(exp2f(end - l0), exp2f(end - l1));
+        };
+        __syncthreads();  // the previous item is done with shared and tensor memory
+        load_v(0);
+        load_k(0);
+        load_v(1);
+        cp_async_commit();
+        if (!issuer)
+            for (int32_t c = warp; c < chunks; c += T / 32) {
+                const float2 g = chunk_decays(p, sg, h, c, lane);
+                const Sum t = warp_total(in_log2(g.x) + in_log2(g.y));
+                if (lane == 0) totals[c] = t;
+            }
+        // the issuing warp works out the factors, a chunk ahead of the terms and two chunks
+        // behind the loads of the decays
+        float2 g = make_float2(0.f, 0.f);
+        __syncthreads();
+        if (issuer) {
+            factors(0, chunk_decays(p, sg, h, 0, lane));
+            g = chunk_decays(p, sg, h, 1, lane);
+        }
+        for (int32_t c = 0; c < chunks; ++c) {
+            if (c == 0) cp_async_wait<0>();
+            else cp_async_wait<1>();
+            fence_proxy_async_smem();
+            bad = __syncthreads_or(bad);  // v and the factors of chunk c are there
+            if (bad) break;
+            const uint32_t terms = S::AT_W + (c & 1) * 3 * S::VB;
+            if (!issuer) {
+                decayed_terms<VD, S::VB, T>(smem + S::AT_V + c % 3 * S::VB, smem + terms, fac + (c & 1) * kChunk, true, tid);
+            } else if (c + 1 < chunks) {
+                factors(c + 1, g);
+                g = chunk_decays(p, sg, h, c + 2, lane);
+            }
+            cp_async_wait<0>();  // k of chunk c
+            fence_proxy_async_smem();
+            tmem_fence_before();
+            __syncthreads();
+            tmem_fence_after();
+            if (issuer) {
+                issue_update<D>(tm, base + terms, base + (c & 1) * S::KB, true, c > 0);
+                tmem_commit(&bars[c & 1]);
+            }
+            // the products of the chunk before are done with its k and terms
+            if (c > 0) wait(c - 1);
+            load_k(c + 1);
+            load_v(c + 2);
+            cp_async_commit();
+        }
+        if (!bad) wait(chunks - 1);
+        bad = __syncthreads_or(bad);
+        if (bad) break;
+        tmem_fence_after();
+        float* dst = p.slots + (static_cast<int64_t>(sg.slot + 1) * p.H + h) * D * D + dv0;
+        if (!issuer) {
+            constexpr int PARTS = T / 128, CW = D / PARTS < 32 ? D / PARTS : 32;
+#pragma unroll
+            for (int b = 0; b < D / PARTS / CW; ++b) {
+                const int c0 = (warp >> 2) * (D / PARTS) + b * CW;
+                uint32_t x[CW];
+                tmem_ld(tm + lanes + c0, x);
+                tmem_ld_wait();
+                if (row < VD)
+#pragma unroll
+                    for (int i = 0; i < CW; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
+            }
+            if (dv0 == 0 && warp == 0) {  // the segment's decay
+                Sum t = {0.f, 0.f};
+                for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
+                t = warp_total(t);
+                if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(t.h);
+            }
+        }
+        tmem_fence_before();
+    }
+    cp_async_wait<0>();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (bad && tid == 0) set_err(p.err, YOCO_DEVERR_TIMEOUT);
+    if (issuer) tmem_dealloc(tm, kTensorCols);
+}
+
+// Outputs, chunk by chunk. Three groups of warps meet three times a chunk:
+//   8 state warps   scale the state and copy it to bf16, then (those whose lanes hold
+//                   tokens) decay P, the others copy the next chunk's k and work out
+//                   factors
+//   8 value warps   work out the terms of v, then copy the next chunk's q and v and write
+//                   the outputs of the chunk before
+//   1 issuing warp  P | O1 and the state's update | O2
+// so that copies, arithmetic, stores and products of one and the next chunk overlap.
+template <int D>
+struct RetOutShape : RetDims<D> {
+    using B = RetDims<D>;
+    static constexpr int STAGE = 2 * B::KB + B::VB;  // q, k, v
+    static constexpr int AT_W = 2 * STAGE, AT_P = AT_W + 3 * B::VB, AT_F = AT_P + kBlockBytes + B::PAD;
+    // of each of 4 chunks, for its 64 tokens t: the running sum L_t (high and low parts, log2
+    // units), exp(L_t), exp(L_end - L_t), exp(L_t - L_mid), exp(L_mid - L_t)
+    static constexpr int FACTORS = 6;
+    // then of each exp(L_C), and whether L_mid serves (the chunk's sums span less than 2^100)
+    static constexpr int SMEM = AT_F + 4 * (FACTORS * kChunk * 4 + 8) + 1024;
+    // tensor memory columns: S^T, its bf16 copy, O1^T, O2^T (and P before it)
+    static constexpr int TS = 0, TC = D, TO1 = D + D / 2, TO2 = TO1 + kChunk;
+    static_assert(TO2 + kChunk <= kTensorCols, "tensor memory");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <int D>
+__global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetParams p) {
+    using S = RetOutShape<D>;
+    constexpr int NS = S::NS, VD = S::VD, F = S::FACTORS * kChunk;
+    constexpr int CW = D / 2 < 32 ? D / 2 : 32;  // columns of a step through a state warp's half
+    constexpr int HT = kChunk / 2;               // tokens of a half of a chunk
+    extern __shared__ uint8_t ret_smem[];
+    __shared__ __align__(8) uint64_t bar_p, bar_o, bar_s;
+    __shared__ uint32_t tmem_base;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ret_smem) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const uint32_t base = smem_u32(smem);
+    float* const fac = reinterpret_cast<float*>(smem + S::AT_F);
+    float2* const whole = reinterpret_cast<float2*>(fac + 4 * F);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool of_state = warp < 8, issuer = warp == 16;
+    const bool loader = of_state && (warp & 2);   // state warps without tokens: 2, 3, 6, 7
+    const int half = (warp >> 2) & 1;             // which half of the columns this warp takes
+    const int row = (warp & 3) * 32 + lane;       // its lane of tensor memory
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    if (tid == 0) {
+        mbar_init(&bar_p, 1);
+        mbar_init(&bar_o, 1);
+        mbar_init(&bar_s, 1);
+        fence_mbar_init();
+    }
+    if (issuer) tmem_alloc(&tmem_base, kTensorCols);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the segments and their states are there
+    // Phases of the barriers. P: waited for by the token warps; O: by the value warps; the
+    // state's update: by the state warps. Each is waited for before the chunk's products that
+    // complete it next are issued.
+    uint32_t ph_p = 0, ph_o = 0, ph_s = 0;
+    bool bad = false;  // a wait has given up
     auto wait = [&](uint64_t* bar, uint32_t& ph) {
         if (!bad && !mbar_wait_bounded(bar, ph, kRetWaitNs)) bad = true;
         ph ^= 1;
-    };
-    auto wait_update = [&](int32_t c) {
-        const int i = OUT ? 0 : c & 1;
-        if (i) wait(&bar_s[1], ph_s[1]);
-        else wait(&bar_s[0], ph_s[0]);
     };
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
 
     for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const RetSeg sg = p.segs[item / (p.H * NS)];
-        const bool last = sg.index == sg.count - 1;
-        if (sg.count == 0 || (!OUT && last)) continue;
+        if (sg.count == 0) continue;
+        const bool last = sg.index == sg.count - 1;  // the state after it leaves the kernel
         const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
-
-        // chunk c into its stage: a thread takes one 16-byte piece of every RS-th row
-        auto load_rows = [&](uint32_t dst, const __nv_bfloat16* src, int64_t stride, int pieces, int32_t left) {
-            const int rs = kChunkThreads / pieces, t0 = tid / pieces, j = tid % pieces;
-            const __nv_bfloat16* at = src + t0 * stride + j * 8;
-            const uint32_t to = dst + block_at(t0, j);  // rs is a multiple of 8: the swizzle stays
-            for (int t = t0; t < kChunk; t += rs) {
-                const bool there = t < left;
-                cp_async_16_or_zero(to + (t - t0) * 128, there ? at : src, there);
-                at += rs * stride;
-            }
-        };
+        // chunk c into its stage: k by the 128 loader threads, q and v by the value warps
         auto load = [&](int32_t c) {
-            if (issuer) return;
-            const uint32_t st = base + c % S::STAGES * S::STAGE;
+            const uint32_t st = base + (c & 1) * S::STAGE;
             const int32_t left = sg.tokens - c * kChunk;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
-            if constexpr (OUT)
-                load_rows(st, p.q + (t0 * p.H + h) * D, static_cast<int64_t>(p.H) * D, D / 8, left);
-            load_rows(st + S::QB, p.k + (t0 * H_kv + hk) * D, static_cast<int64_t>(H_kv) * D, D / 8, left);
-            load_rows(st + S::QB + S::KB, p.v + (t0 * H_kv + hk) * D + dv0, static_cast<int64_t>(H_kv) * D, VD / 8, left);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (of_state) {
+                load_rows<D / 8, 128>(st + S::KB, p.k + (t0 * H_kv + hk) * D, static_cast<int64_t>(H_kv) * D, left,
+                                      (half * 2 + (warp & 1)) * 32 + lane);
+            } else {
+                load_rows<D / 8, 256>(st, p.q + (t0 * p.H + h) * D, static_cast<int64_t>(p.H) * D, left, tid - 256);
+                load_rows<VD / 8, 256>(st + 2 * S::KB, p.v + (t0 * H_kv + hk) * D + dv0, static_cast<int64_t>(H_kv) * D,
+                                       left, tid - 256);
+            }
+            cp_async_commit();
+        };
+        const bool copies = loader || (!of_state && !issuer);
+        auto factors = [&](int32_t c, float2 g) {  // from the chunk's decays: one warp
+            Sum l0, l1;
+            running_sums(g, lane, l0, l1);
+            auto of_lane = [](Sum a, int l) {
+                return Sum{__shfl_sync(0xffffffffu, a.h, l), __shfl_sync(0xffffffffu, a.l, l)};
+            };
+            const Sum end = of_lane(l1, 31), first = of_lane(l0, 0), mid = of_lane(l0, 16);
+            auto put = [&](int i, float x, float y) {
+                *reinterpret_cast<float2*>(fac + (c & 3) * F + i * kChunk + 2 * lane) = make_float2(x, y);
+            };
+            put(0, l0.h, l1.h);
+            put(1, l0.l, l1.l);
+            put(2, exp2f(l0.h), exp2f(l1.h));
+            put(3, exp2f(end - l0), exp2f(end - l1));
+            put(4, exp2f(l0 - mid), exp2f(l1 - mid));
+            put(5, exp2f(mid - l0), exp2f(mid - l1));
+            if (lane == 0) whole[c & 3] = make_float2(exp2f(end.h), fabsf(first - end) < 100.f ? 1.f : 0.f);
         };
         __syncthreads();  // the previous item is done with shared and tensor memory
-        load(0);
-        if (S::STAGES == 3 && chunks > 1) load(1);
-
-        // log decays of chunk cc: lane l has tokens 2l and 2l + 1
-        auto decays = [&](int32_t cc, Sum& g0, Sum& g1) {
-            const int64_t t0 = sg.token + static_cast<int64_t>(cc) * kChunk;
-            const int32_t left = cc < chunks ? min(kChunk, sg.tokens - cc * kChunk) : 0;
-            g0 = 2 * lane < left ? in_log2(decay_of(p, t0 + 2 * lane, h)) : Sum{0.f, 0.f};
-            g1 = 2 * lane + 1 < left ? in_log2(decay_of(p, t0 + 2 * lane + 1, h)) : Sum{0.f, 0.f};
-        };
-        if constexpr (OUT) {  // the state before the segment
+        if (copies) load(0);
+        if (warp == 8) factors(0, chunk_decays(p, sg, h, 0, lane));
+        if (warp == 9 && chunks > 1) factors(1, chunk_decays(p, sg, h, 1, lane));
+        float2 g = make_float2(0.f, 0.f);  // warps 2 and 3: decays of the next even and odd chunk
+        if (of_state) {  // the state before the segment
             const float* src = nullptr;
             const int32_t q = __ldg(p.qsl + sg.req + 1) - __ldg(p.qsl + sg.req);
             if (sg.slot >= 0)
@@ -498,293 +746,209 @@ __global__ void __launch_bounds__(kChunkThreads + 32, 1) retention_chunks(const 
             else if (__ldg(p.seq_lens + sg.req) > q)
                 src = p.state + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
             if (row >= VD) src = nullptr;
-            if (!issuer) {
 #pragma unroll
-                for (int b = 0; b < D / 64; ++b) {
-                    const int c0 = half * (D / 2) + b * 32;
-                    uint32_t x[32];
+            for (int b = 0; b < D / 2 / CW; ++b) {
+                const int c0 = half * (D / 2) + b * CW;
+                uint32_t x[CW];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = src ? __float_as_uint(src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
-                    tmem_st32(tm + lanes + S::TS + c0, x);
-                }
-                tmem_st_wait();
+                for (int i = 0; i < CW; ++i)
+                    x[i] = src ? __float_as_uint(src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
+                tmem_st(tm + lanes + S::TS + c0, x);
             }
-        } else {  // decay sums of the segment's chunks
-            if (!issuer)
-                for (int32_t cc = warp; cc < chunks; cc += 8) {
-                    Sum g0, g1;
-                    decays(cc, g0, g1);
-                    const Sum t = warp_total(g0 + g1);
-                    if (lane == 0) totals[cc] = t;
-                }
-            __syncthreads();
+            tmem_st_wait();
         }
         bool pending = false;  // an update of the state is under way
+        uint32_t y[HT / 2];    // value warps: outputs of the chunk before, two tokens a word
+        auto take_outputs = [&](int32_t c) {  // of chunk c, from tensor memory
+            wait(&bar_o, ph_o);
+            tmem_fence_after();
+            const float* et = fac + (c & 3) * F + 2 * kChunk + half * HT;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                uint32_t o1[16], o2[16];
+                tmem_ld(tm + lanes + S::TO1 + half * HT + b * 16, o1);
+                tmem_ld(tm + lanes + S::TO2 + half * HT + b * 16, o2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int t = 0; t < 16; t += 2) {
+                    const float2 e = *reinterpret_cast<const float2*>(et + b * 16 + t);
+                    y[b * 8 + t / 2] =
+                        pack_bf16x2(p.scale * fmaf(e.x, __uint_as_float(o1[t]), __uint_as_float(o2[t])),
+                                    p.scale * fmaf(e.y, __uint_as_float(o1[t + 1]), __uint_as_float(o2[t + 1])));
+                }
+            }
+        };
+        auto write_outputs = [&](int32_t c) {
+            // two lanes exchange, so that each writes two value dims of every other token: a
+            // warp's 32 lanes are 64 bytes of two tokens' rows
+            const int odd = lane & 1;
+            const int32_t left = sg.tokens - c * kChunk - half * HT - odd;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + half * HT + odd) * p.H + h) * D + dv0 + (row & ~1));
+            const int64_t step = static_cast<int64_t>(p.H) * D;  // two tokens on, in words
+#pragma unroll
+            for (int t = 0; t < HT; t += 2) {
+                const uint32_t z = __shfl_xor_sync(0xffffffffu, y[t / 2], 1);
+                if (row < VD && t < left) *dst = odd ? __byte_perm(z, y[t / 2], 0x7632) : __byte_perm(y[t / 2], z, 0x5410);
+                dst += step;
+            }
+        };
 
         for (int32_t c = 0; c < chunks; ++c) {
-            if (c % S::FG == 0) {  // running sums and factors of the next chunks, one a warp
-                if (c) __syncthreads();
-                if (warp < S::FG) {
-                    const int32_t cc = c + warp;
-                    Sum g0, g1;
-                    decays(cc, g0, g1);
-                    Sum l1 = g0 + g1;
-#pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const Sum x = shfl_up(l1, off);
-                        if (lane >= off) l1 = l1 + x;
-                    }
-                    const Sum l0 = l1 + Sum{-g1.h, -g1.l};
-                    auto of_lane = [](Sum a, int l) {
-                        return Sum{__shfl_sync(0xffffffffu, a.h, l), __shfl_sync(0xffffffffu, a.l, l)};
-                    };
-                    const Sum total = of_lane(l1, 31);
-                    Sum end = total;
-                    if constexpr (!OUT) {  // to the end of the segment
-                        Sum t = {0.f, 0.f};
-                        for (int32_t x = cc + 1 + lane; x < chunks; x += 32) t = t + totals[x];
-                        end = end + warp_total(t);
-                    }
-                    auto put = [&](int i, float x, float y) {
-                        *reinterpret_cast<float2*>(fac + (warp * kFactors + i) * kChunk + 2 * lane) = make_float2(x, y);
-                    };
-                    put(3, exp2f(end - l0), exp2f(end - l1));
-                    if constexpr (OUT) {
-                        const Sum first = of_lane(l0, 0), mid = of_lane(l0, 16);
-                        put(0, l0.h, l1.h);
-                        put(1, l0.l, l1.l);
-                        put(2, exp2f(l0.h), exp2f(l1.h));
-                        put(4, exp2f(l0 - mid), exp2f(l1 - mid));
-                        put(5, exp2f(mid - l0), exp2f(mid - l1));
-                        if (lane == 0) whole[warp] = make_float2(exp2f(total.h), fabsf(first - total) < 100.f ? 1.f : 0.f);
-                    }
-                }
+            const uint32_t at = (c & 1) * S::STAGE;  // of the chunk's q, k, v
+            const uint32_t sq = base + at, sk = sq + S::KB, sv = sk + S::KB;
+            const float* f = fac + (c & 3) * F;
+            const bool update = last || c + 1 < chunks;
+            if (copies) {
+                cp_async_wait<0>();
+                fence_proxy_async_smem();
             }
-            const uint32_t at = c % S::STAGES * S::STAGE;  // of the chunk's q, k, v
-            const uint32_t sq = base + at, sk = sq + S::QB, sv = sk + S::KB;
-            const uint32_t aw = AT_W + (S::WBUF == 2 ? (c & 1) * S::TERMS : 0);
-            const float* f = fac + c % S::FG * kFactors * kChunk;
-            const bool update = !OUT || last || c + 1 < chunks;
-            const bool three = !OUT || last;  // terms of the decayed v
-
-            if (S::STAGES == 3 && c + 1 < chunks) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else asm volatile("cp.async.wait_group 0;" ::: "memory");
-            fence_proxy_async_smem();
-            // the state before this chunk is complete (with one set of terms: they are free)
-            if (S::WBUF == 1 && pending) wait_update(c - 1);
+            if (of_state && pending) wait(&bar_s, ph_s);  // the state before this chunk is complete
+            pending = update;
+            if (!of_state && !issuer && c > 0) take_outputs(c - 1);
             tmem_fence_before();
-            bad = __syncthreads_or(bad);  // chunk c and its factors are in shared memory
+            bad = __syncthreads_or(bad);  // (1) chunk c, its factors and its place are there
             if (bad) break;
             tmem_fence_after();
-            if (!OUT && S::WBUF == 1 && c + 2 < chunks) load(c + 2);
-            if (OUT && c + 1 < chunks) load(c + 1);
-            if (issuer) {
-                if constexpr (OUT) {  // P = q k^T (128 rows: the upper 64 are not looked at)
+            if (issuer) {  // P = q k^T (128 rows: the upper 64 are not looked at)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
-                        tmem_mma(tm + S::TO2, smem_operand(sq + o, 16, 1024), smem_operand(sk + o, 16, 1024),
-                                 bf16_product(128, kChunk, false, false), kk > 0);
-                    }
-                    tmem_commit(&bar_p);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * kBlockBytes + (kk & 3) * 32;
+                    tmem_mma(tm + S::TO2, smem_operand(sq + o, 16, 1024), smem_operand(sk + o, 16, 1024),
+                             bf16_product(128, kChunk, false, false), kk > 0);
                 }
-            } else {
-                if (update) {  // exp(L_end - L_j) v_j in bf16 terms, each cut from what the ones before leave
+                tmem_commit(&bar_p);
+            } else if (of_state) {  // the state as a bf16 operand, then scaled by the chunk's decay
+                const float aC = whole[c & 3].x;
 #pragma unroll
-                    for (int x = tid; x < kChunk * (VD / 8); x += kChunkThreads) {
-                        const int t = x / (VD / 8), j = x % (VD / 8);
-                        const uint32_t o = block_at(t, j);
-                        const uint4 w = *reinterpret_cast<const uint4*>(smem + at + S::QB + S::KB + o);
-                        const float fw = f[3 * kChunk + t];
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t r[3][4];
+                for (int b = 0; b < D / 2 / CW; ++b) {
+                    const int c0 = half * (D / 2) + b * CW;
+                    uint32_t x[CW], z[CW / 2];
+                    tmem_ld(tm + lanes + S::TS + c0, x);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < CW / 2; ++i) {
+                        z[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                        x[2 * i] = __float_as_uint(__uint_as_float(x[2 * i]) * aC);
+                        x[2 * i + 1] = __float_as_uint(__uint_as_float(x[2 * i + 1]) * aC);
+                    }
+                    tmem_st(tm + lanes + S::TC + c0 / 2, z);
+                    if (update) tmem_st(tm + lanes + S::TS + c0, x);
+                }
+                tmem_st_wait();
+            } else if (update) {
+                decayed_terms<VD, S::VB, 256>(smem + at + 2 * S::KB, smem + S::AT_W, f + 3 * kChunk, last, tid - 256);
+                fence_proxy_async_smem();
+            }
+            tmem_fence_before();
+            __syncthreads();  // (2) the state's copy and the terms are complete
+            tmem_fence_after();
+            if (issuer) {  // O1^T = S^T q^T, and the state after the chunk
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tmem_mma_ta(tm + S::TO1, tm + S::TC + kk * 8,
+                                smem_operand(sq + (kk >> 2) * kBlockBytes + (kk & 3) * 32, 16, 1024),
+                                bf16_product(128, kChunk, false, false), kk > 0);
+                if (update) {
+                    issue_update<D>(tm + S::TS, base + S::AT_W, sk, last, true);
+                    tmem_commit(&bar_s);
+                }
+            } else if (!of_state) {
+                if (c + 1 < chunks) load(c + 1);
+                if (c > 0) write_outputs(c - 1);
+            } else if (loader) {
+                if (c + 1 < chunks) load(c + 1);  // its stage: the products of chunk c - 1 are done
+                if (warp < 4) {  // factors of two chunks every other one, from decays loaded the time before
+                    const int32_t x = c + (c & 1 ? 1 : 2) + (warp & 1);
+                    if (!(c & 1)) g = chunk_decays(p, sg, h, x, lane);
+                    else if (x < chunks) factors(x, g);
+                }
+            } else {  // weights of token `row` for 32 tokens
+                wait(&bar_p, ph_p);
+                tmem_fence_after();
+                uint8_t* dst = smem + S::AT_P;
+                if ((warp & 3) < half) {  // all later tokens
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4*>(dst + block_at(row, half * 4 + i)) = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    uint32_t x[HT];
+                    tmem_ld(tm + lanes + S::TO2 + half * HT, x);
+                    tmem_ld_wait();
+                    const bool near = whole[c & 3].y != 0.f, diagonal = (warp & 3) == half;
+                    const float th = f[row], tl = f[kChunk + row], tf = f[4 * kChunk + row];
+#pragma unroll
+                    for (int q4 = 0; q4 < HT / 4; ++q4) {
+                        const int j0 = half * HT + q4 * 4;
+                        float w[4];
+                        if (near) {  // one factor of the row, one of the column
+                            const float4 m = *reinterpret_cast<const float4*>(f + 5 * kChunk + j0);
+                            w[0] = tf * m.x;
+                            w[1] = tf * m.y;
+                            w[2] = tf * m.z;
+                            w[3] = tf * m.w;
+                        } else {
+                            const float4 jh = *reinterpret_cast<const float4*>(f + j0);
+                            const float4 jl = *reinterpret_cast<const float4*>(f + kChunk + j0);
+                            w[0] = exp2_approx((th - jh.x) + (tl - jl.x));
+                            w[1] = exp2_approx((th - jh.y) + (tl - jl.y));
+                            w[2] = exp2_approx((th - jh.z) + (tl - jl.z));
+                            w[3] = exp2_approx((th - jh.w) + (tl - jl.w));
+                        }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float lo = bf16lo_to_f32(in[i]) * fw, hi = bf16hi_to_f32(in[i]) * fw;
-#pragma unroll
-                            for (int u = 0; u < 3; ++u) {
-                                r[u][i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-                                lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
-                                hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
-                            }
+                            w[i] *= __uint_as_float(x[q4 * 4 + i]);
+                            if (diagonal && j0 + i > row) w[i] = 0.f;
                         }
-#pragma unroll
-                        for (int u = 0; u < 3; ++u)
-                            if (u < 2 || three)
-                                *reinterpret_cast<uint4*>(smem + aw + u * S::VB + o) =
-                                    make_uint4(r[u][0], r[u][1], r[u][2], r[u][3]);
-                    }
-                }
-                if constexpr (OUT) {  // the state as a bf16 operand, then scaled by the chunk's decay
-                    const float aC = whole[c % S::FG].x;
-#pragma unroll
-                    for (int b = 0; b < D / 64; ++b) {
-                        const int c0 = half * (D / 2) + b * 32;
-                        uint32_t x[32], y[16];
-                        tmem_ld32(tm + lanes + S::TS + c0, x);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            y[i] = pack_bf16x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                            x[2 * i] = __float_as_uint(__uint_as_float(x[2 * i]) * aC);
-                            x[2 * i + 1] = __float_as_uint(__uint_as_float(x[2 * i + 1]) * aC);
-                        }
-                        tmem_st16(tm + lanes + S::TC + c0 / 2, y);
-                        if (update) tmem_st32(tm + lanes + S::TS + c0, x);
-                    }
-                    tmem_st_wait();
-                }
-            }
-            fence_proxy_async_smem();
-            tmem_fence_before();
-            __syncthreads();  // the state's copy and the terms are complete
-            tmem_fence_after();
-            if constexpr (OUT) {
-                if (issuer) {  // O1^T = S^T q^T
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk)
-                        tmem_mma_ta(tm + S::TO1, tm + S::TC + kk * 8,
-                                    smem_operand(sq + (kk >> 2) * kBlockBytes + (kk & 3) * 32, 16, 1024),
-                                    bf16_product(128, kChunk, false, false), kk > 0);
-                    ph_p ^= 1;
-                } else {
-                    wait(&bar_p, ph_p);
-                    tmem_fence_after();
-                    if (row < kChunk) {  // warps 0, 1, 4, 5: weights of token `row`, 32 earlier tokens
-                        uint32_t x[32];
-                        tmem_ld32(tm + lanes + S::TO2 + half * 32, x);
-                        tmem_ld_wait();
-                        const bool near = whole[c % S::FG].y != 0.f;
-                        const float th = f[row], tl = f[kChunk + row], tm_ = f[4 * kChunk + row];
-#pragma unroll
-                        for (int q4 = 0; q4 < 8; ++q4) {
-                            const int j0 = half * 32 + q4 * 4;
-                            float w[4];
-                            if (near) {  // one factor of the row, one of the column
-                                const float4 m = *reinterpret_cast<const float4*>(f + 5 * kChunk + j0);
-                                w[0] = tm_ * m.x;
-                                w[1] = tm_ * m.y;
-                                w[2] = tm_ * m.z;
-                                w[3] = tm_ * m.w;
-                            } else {
-                                const float4 jh = *reinterpret_cast<const float4*>(f + j0);
-                                const float4 jl = *reinterpret_cast<const float4*>(f + kChunk + j0);
-                                w[0] = exp2_approx((th - jh.x) + (tl - jl.x));
-                                w[1] = exp2_approx((th - jh.y) + (tl - jl.y));
-                                w[2] = exp2_approx((th - jh.z) + (tl - jl.z));
-                                w[3] = exp2_approx((th - jh.w) + (tl - jl.w));
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                w[i] = j0 + i <= row ? w[i] * __uint_as_float(x[q4 * 4 + i]) : 0.f;
-                            *reinterpret_cast<uint2*>(smem + AT_P + block_at(row, half * 4 + (q4 >> 1)) + (q4 & 1) * 8) =
-                                make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
-                        }
+                        *reinterpret_cast<uint2*>(dst + block_at(row, half * 4 + (q4 >> 1)) + (q4 & 1) * 8) =
+                            make_uint2(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]));
                     }
                 }
                 fence_proxy_async_smem();
-                tmem_fence_before();
-                __syncthreads();  // P is in shared memory, its columns are free
-                tmem_fence_after();
             }
-            if (issuer) {
-                if constexpr (OUT) {  // O2^T = v^T P^T
+            tmem_fence_before();
+            __syncthreads();  // (3) P is in shared memory, its columns are free
+            tmem_fence_after();
+            if (issuer) {  // O2^T = v^T P^T
 #pragma unroll
-                    for (int kk = 0; kk < kChunk / 16; ++kk)
-                        tmem_mma(tm + S::TO2, smem_operand(sv + kk * 2048, kBlockBytes, 1024),
-                                 smem_operand(base + AT_P + kk * 32, 16, 1024), bf16_product(128, kChunk, true, false),
-                                 kk > 0);
-                    tmem_commit(&bar_o);
-                    ph_o ^= 1;
-                }
-                if (update) {  // S^T += (decayed v)^T k
-#pragma unroll
-                    for (int u = 0; u < 3; ++u)
-                        if (u < 2 || three)
-#pragma unroll
-                            for (int kk = 0; kk < kChunk / 16; ++kk)
-                                tmem_mma(tm + S::TS, smem_operand(base + aw + u * S::VB + kk * 2048, kBlockBytes, 1024),
-                                         smem_operand(sk + kk * 2048, kBlockBytes, 1024),
-                                         bf16_product(128, D, true, true), OUT || c > 0 || u > 0 || kk > 0);
-                    tmem_commit(&bar_s[OUT ? 0 : c & 1]);
-                }
-            }
-            if constexpr (OUT) {
-                pending = update;
-                if (!issuer) {
-                    wait(&bar_o, ph_o);
-                    tmem_fence_after();
-                    uint32_t a[32], b[32];
-                    tmem_ld32(tm + lanes + S::TO1 + half * 32, a);
-                    tmem_ld32(tm + lanes + S::TO2 + half * 32, b);
-                    tmem_ld_wait();
-                    // to rows of tokens, in the place of the chunk's q, whose products are done
-                    const float* et = f + 2 * kChunk + half * 32;
-                    uint8_t* to = smem + at + half * 32 * (2 * VD) + 2 * row;
-                    if (row < VD) {
-#pragma unroll
-                        for (int t = 0; t < 32; ++t)
-                            *reinterpret_cast<__nv_bfloat16*>(to + t * (2 * VD)) = __float2bfloat16_rn(
-                                p.scale * fmaf(et[t], __uint_as_float(a[t]), __uint_as_float(b[t])));
-                    }
-                    asm volatile("bar.sync 1, %0;" ::"n"(kChunkThreads) : "memory");  // all but the issuer
-                    const int32_t left = sg.tokens - c * kChunk;
-                    constexpr int J = VD / 8, RS = kChunkThreads / J;
-                    const int t0 = tid / J, j = tid % J;
-                    const uint8_t* from = smem + at + t0 * (2 * VD) + j * 16;
-                    __nv_bfloat16* dst =
-                        p.out + ((sg.token + static_cast<int64_t>(c) * kChunk + t0) * p.H + h) * D + dv0 + j * 8;
-#pragma unroll
-                    for (int t = 0; t < kChunk; t += RS) {
-                        if (t0 + t < left)
-                            *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(from + t * (2 * VD));
-                        dst += static_cast<int64_t>(RS) * p.H * D;
-                    }
-                }
-            } else {
-                // the products of the chunk before are done with its stage and terms
-                if (S::WBUF == 2 && pending) wait_update(c - 1);
-                pending = true;
-                if (S::WBUF == 2 && c + 2 < chunks) load(c + 2);
+                for (int kk = 0; kk < kChunk / 16; ++kk)
+                    tmem_mma(tm + S::TO2, smem_operand(sv + kk * 2048, kBlockBytes, 1024),
+                             smem_operand(base + S::AT_P + kk * 32, 16, 1024), bf16_product(128, kChunk, true, false),
+                             kk > 0);
+                tmem_commit(&bar_o);
             }
         }
-        if (!bad && pending) wait_update(chunks - 1);
+        if (!bad) {
+            if (of_state && pending) wait(&bar_s, ph_s);
+            if (!of_state && !issuer) {
+                take_outputs(chunks - 1);
+                write_outputs(chunks - 1);
+            }
+        }
         bad = __syncthreads_or(bad);
         if (bad) break;
         tmem_fence_after();
-        // the state after the segment
-        float* dst = nullptr;
-        if (!OUT)
-            dst = p.slots + (static_cast<int64_t>(sg.slot + 1) * p.H + h) * D * D + dv0;
-        else if (last)
-            dst = p.state_out + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
-        if (dst && !issuer) {
+        if (last && of_state) {  // the state after the request
+            float* dst = p.state_out + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
 #pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                const int c0 = half * (D / 2) + b * 32;
-                uint32_t x[32];
-                tmem_ld32(tm + lanes + S::TS + c0, x);
+            for (int b = 0; b < D / 2 / CW; ++b) {
+                const int c0 = half * (D / 2) + b * CW;
+                uint32_t x[CW];
+                tmem_ld(tm + lanes + S::TS + c0, x);
                 tmem_ld_wait();
                 if (row < VD)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
+                    for (int i = 0; i < CW; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
             }
-        }
-        if (!OUT && dv0 == 0 && warp == 0) {  // the segment's decay
-            Sum t = {0.f, 0.f};
-            for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
-            t = warp_total(t);
-            if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(t.h);
         }
         tmem_fence_before();
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    cp_async_wait<0>();
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     if (bad && tid == 0) set_err(p.err, YOCO_DEVERR_TIMEOUT);
-    if (issuer) tmem_dealloc(tm, S::TCOLS);
+    if (issuer) tmem_dealloc(tm, kTensorCols);
 }
 
 // ------------------------------------------------------------------ host side
@@ -857,32 +1021,44 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
         if (e != cudaSuccess || p.seg_tokens == 0) return e;
     }
     static unsigned long long done_out = 0, done_add = 0;
-    e = ret_smem_attr(retention_chunks<D, true>, RetShape<D, true>::SMEM, done_out);
-    if (e == cudaSuccess) e = ret_smem_attr(retention_chunks<D, false>, RetShape<D, false>::SMEM, done_add);
+    e = ret_smem_attr(retention_out<D>, RetOutShape<D>::SMEM, done_out);
+    if (e == cudaSuccess) e = ret_smem_attr(retention_add<D>, RetAddShape<D>::SMEM, done_add);
     if (e != cudaSuccess) return e;
-    const int sms = device_sm_count(), units = p.H * RetShape<D, true>::NS;
+    const int sms = device_sm_count(), units = p.H * RetDims<D>::NS;
     const int64_t items = static_cast<int64_t>(p.max_segs) * units;
     const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);  // one CTA an SM
     retention_plan<<<1, 1024, 0, s>>>(p, units, sms);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // The chunk passes start while the kernel before them ends (they wait for it before
+    // they read), single tokens beside the segments' pass: bound by HBM next to products.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (cut) {
-        retention_chunks<D, false><<<grid, kChunkThreads + 32, RetShape<D, false>::SMEM, s>>>(p);
-        // single tokens: bound by HBM, they run beside the segments' products
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kAddThreads + 32);
+        cfg.dynamicSmemBytes = RetAddShape<D>::SMEM;
+        e = cudaLaunchKernelEx(&cfg, retention_add<D>, p);
+        if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(steps);
         cfg.blockDim = dim3(256);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+        cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, retention_step<D>, p);
         if (e != cudaSuccess) return e;
         const int64_t parts = static_cast<int64_t>(p.max_segs) * p.H * (D * D / 1024);
         retention_scan<D><<<static_cast<unsigned>(parts < 16 * sms ? parts : 16 * sms), 256, 0, s>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
     }
-    retention_chunks<D, true><<<grid, kChunkThreads + 32, RetShape<D, true>::SMEM, s>>>(p);
-    return cudaGetLastError();
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kOutThreads + 32);
+    cfg.dynamicSmemBytes = RetOutShape<D>::SMEM;
+    return cudaLaunchKernelEx(&cfg, retention_out<D>, p);
 }
 
 bool ret_shape_ok(int32_t H, int32_t D) {
