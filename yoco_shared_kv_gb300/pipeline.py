@@ -7,6 +7,9 @@ K^/V^ pools, metadata, per-layer queries and outputs) and runs the path:
     yoco_select_cross_rows  (rows entering the cross-decoder)
     yoco_cross_attn_paged   x layers (each layer's own queries, same cache)
 
+(over a quantised cache their _e4m3 or _e2m1 forms, the latter after
+yoco_build_block_tables has given every token its slot)
+
 as in "YOCO 论文与推理数据流详解" §13.4 (self-prefill, global-KV finalize,
 cross-decode) and "You Only Cache Once, in vLLM" (cross-decoder batch =
 one row per scheduled request). Only allocation and argument marshalling
@@ -33,10 +36,15 @@ def torch_dtype(dtype: str) -> torch.dtype:
     return {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
 
 
+def cache_dtype(wl, kv: str) -> torch.dtype:
+    """The dtype that names a workload's cache to the library."""
+    return {"e4m3": torch.float8_e4m3fn, "e2m1": N.E2M1}.get(kv) or torch_dtype(wl.dtype)
+
+
 class DeviceStep:
     """Device copies of one step's inputs, plus its outputs and scratch."""
 
-    def __init__(self, wl, step, device, pin_host: bool = False, e4m3: bool = False):
+    def __init__(self, wl, step, device, pin_host: bool = False, kv: str = "native"):
         self.wl, self.step = wl, step
         dev = torch.device(device)
         i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32))  # noqa: E731
@@ -62,6 +70,8 @@ class DeviceStep:
         self.row_indices = torch.zeros(max(T, 1), dtype=torch.int32, device=dev)
         self.cqsl = torch.zeros(R + 1, dtype=torch.int32, device=dev)
         self.num_rows = torch.zeros(1, dtype=torch.int32, device=dev)
+        # e2m1: every token's slot, worked out on the GPU from the block table
+        self.slots = torch.zeros(T, dtype=torch.int32, device=dev) if kv == "e2m1" else None
         self.out = None
         self.workspace = None
         if step.q is not None:
@@ -69,7 +79,7 @@ class DeviceStep:
             ws = N.yoco_cross_attn_workspace_size(
                 max(self.rows_upper, 1), wl.num_q_heads, wl.num_kv_heads, wl.head_dim,
                 wl.block_size, self.max_seq_len,
-                torch.float8_e4m3fn if e4m3 else torch_dtype(wl.dtype))
+                cache_dtype(wl, kv))
             # all-ones bytes (NaN as fp32): the library must never read scratch it
             # did not write in the same call, and this makes such a read visible
             self.workspace = torch.full((max(ws, 16),), 255, dtype=torch.uint8, device=dev)
@@ -85,20 +95,31 @@ class DeviceStep:
 
 class DeviceWorkload:
     """``kv="e4m3"`` keeps the cache as e4m3 bytes with per-(page, kv head) scale
-    records ``page_scales`` (float32 numpy ``[num_blocks, H_kv, 4]``); the
-    workload's values must then be bf16."""
+    records ``page_scales`` (float32 numpy ``[num_blocks, H_kv, 4]``), ``kv="e2m1"``
+    as 4-bit codes with a scale byte for 32 head dims (``block_scales``, made by the
+    append); the workload's values must then be bf16."""
 
     def __init__(self, wl, device="cuda", pin_host: bool = False, sentinel: bool = True,
                  alternate="auto", kv: str = "native", page_scales=None):
         self.wl = wl
         self.device = torch.device(device)
-        self.e4m3 = kv == "e4m3"
-        if kv not in ("native", "e4m3"):
+        self.kv = kv
+        self.e4m3, self.e2m1 = kv == "e4m3", kv == "e2m1"
+        if kv not in ("native", "e4m3", "e2m1"):
             raise ValueError(kv)
         tdt = torch_dtype(wl.dtype)
         shape = wl.pool_shape()
-        self.page_scales = None
-        if self.e4m3:
+        self.page_scales = self.block_scales = None
+        if self.e2m1:
+            if wl.dtype != "bf16":
+                raise ValueError("the e2m1 cache takes bf16 values")
+            fill = 0xFF if sentinel else 0
+            nb, H, bs, D = shape
+            self.k_cache = torch.full((nb, H, bs, D // 2), fill, dtype=torch.uint8, device=self.device)
+            self.v_cache = torch.full((nb, H, bs, D // 2), fill, dtype=torch.uint8, device=self.device)
+            self.block_scales = torch.full((nb, H, 2, bs, D // 32), fill, dtype=torch.uint8,
+                                           device=self.device)
+        elif self.e4m3:
             if wl.dtype != "bf16":
                 raise ValueError("the e4m3 cache takes bf16 values")
             if page_scales is None:
@@ -125,14 +146,20 @@ class DeviceWorkload:
             l2 = torch.cuda.get_device_properties(self.device).L2_cache_size
             alternate = pool_bytes > l2
         self.alternate = bool(alternate)
-        e8 = self.e4m3
-        self.fill = DeviceStep(wl, wl.fill, device, pin_host, e8) if wl.fill is not None else None
-        self.steps: List[DeviceStep] = [DeviceStep(wl, s, device, pin_host, e8) for s in wl.steps]
+        self.fill = DeviceStep(wl, wl.fill, device, pin_host, kv) if wl.fill is not None else None
+        self.steps: List[DeviceStep] = [DeviceStep(wl, s, device, pin_host, kv) for s in wl.steps]
 
     # ------------------------------------------------------------------ calls
 
     def append(self, ds: DeviceStep, stream=None) -> None:
         d = ds.dev
+        if self.e2m1:
+            N.yoco_build_block_tables(d["block_table"], d["seq_lens"], d["qsl"],
+                                      self.k_cache.shape[0], self.wl.block_size, ds.slots,
+                                      err_word=self.err, stream=stream)
+            N.yoco_kv_append_e2m1(d["k_new"], d["v_new"], self.k_cache, self.v_cache,
+                                  self.block_scales, ds.slots, self.err, stream)
+            return
         if self.e4m3:
             N.yoco_kv_append_e4m3(d["k_new"], d["v_new"], self.k_cache, self.v_cache,
                                   self.page_scales, d["block_table"], d["seq_lens"], d["qsl"],
@@ -154,8 +181,7 @@ class DeviceWorkload:
         N.yoco_cross_attn_plan(d["block_table"], d["seq_lens"], ds.cqsl if cq is None else cq,
                                ds.max_seq_len, ds.out.shape[1], wl.num_q_heads, wl.num_kv_heads,
                                wl.head_dim, wl.block_size, self.k_cache.shape[0],
-                               torch.float8_e4m3fn if self.e4m3 else torch_dtype(wl.dtype),
-                               ds.workspace, self.err, stream)
+                               cache_dtype(wl, self.kv), ds.workspace, self.err, stream)
 
     def attend(self, ds: DeviceStep, layer: int, stream=None, q: Optional[torch.Tensor] = None,
                out: Optional[torch.Tensor] = None, cq: Optional[torch.Tensor] = None,
@@ -174,9 +200,11 @@ class DeviceWorkload:
             flags |= N.YOCO_ATTN_OVERLAP
         if planned:  # the step's plan (plan() or the fused step) is in the workspace
             flags |= N.YOCO_ATTN_PLANNED
-        if self.e4m3:
-            N.yoco_cross_attn_paged_e4m3(
-                d["q"][layer] if q is None else q, self.k_cache, self.v_cache, self.page_scales,
+        if self.e4m3 or self.e2m1:
+            call = N.yoco_cross_attn_paged_e4m3 if self.e4m3 else N.yoco_cross_attn_paged_e2m1
+            call(
+                d["q"][layer] if q is None else q, self.k_cache, self.v_cache,
+                self.page_scales if self.e4m3 else self.block_scales,
                 ds.out[layer] if out is None else out, d["block_table"], d["seq_lens"],
                 ds.cqsl if cq is None else cq, ds.max_seq_len, self.wl.scale, ds.workspace,
                 self.err, stream, flags=flags)
@@ -192,19 +220,22 @@ class DeviceWorkload:
         qsl = np.asarray(st.query_start_loc)
         rpr = st.rows_per_req
         return bool((np.diff(qsl) == 1).all() and (rpr is None or (np.asarray(rpr) == 1).all())
-                    and self.wl.dtype == "bf16")
+                    and self.wl.dtype == "bf16" and not self.e2m1)
 
     def step_buffers(self, i: int, pin_host: bool = True) -> DeviceStep:
         """Another set of device buffers (inputs, outputs, scratch) for step i, so that
         one set's inputs can be copied in while a step runs on the other."""
-        return DeviceStep(self.wl, self.wl.steps[i], self.device, pin_host, self.e4m3)
+        return DeviceStep(self.wl, self.wl.steps[i], self.device, pin_host, self.kv)
 
     def fused_step(self, i: int, stream=None, layers: Optional[int] = None) -> None:
         self.fused_step_on(self.steps[i], stream, layers)
 
     def fused_step_on(self, ds: DeviceStep, stream=None, layers: Optional[int] = None) -> None:
         """A decode step with the append fused into layer 0 (yoco_cross_decode_step),
-        then every later layer; the row selection is the identity for decode."""
+        then every later layer; the row selection is the identity for decode. Not over
+        an e2m1 cache (the library has no fused step for it)."""
+        if self.e2m1:
+            raise ValueError("the fused step takes a bf16 or e4m3 cache")
         d = ds.dev
         N.yoco_cross_decode_step(d["q"][0], d["k_new"], d["v_new"], self.k_cache, self.v_cache,
                                  self.page_scales, ds.out[0], d["block_table"], d["seq_lens"],
