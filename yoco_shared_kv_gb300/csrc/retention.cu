@@ -16,13 +16,13 @@
 //   retention_step: requests of one token. Moves the state once (read and
 //     write, fp32): bound by HBM.
 //   retention_plan: cuts the longer requests into segments of whole chunks.
-//   retention_add: the state that each segment but a request's
-//     last adds (from zero), all segments at once.
+//   retention_add<false>: the state that each segment adds (from zero), all
+//     segments at once.
 //   retention_scan: runs along a request's segments and turns those into the
-//     state before each segment.
-//   retention_out: outputs of every segment, chunk by chunk, and
-//     the state after a request's last one.
-// A request of one segment needs neither the second pass nor the scan.
+//     state before each segment and after the last.
+//   retention_out: outputs of every segment, chunk by chunk.
+//   retention_add<true>: the state after requests of one segment that the
+//     workspace had no room for in the first pass.
 #include "common.cuh"
 
 namespace yoco {
@@ -59,7 +59,7 @@ struct RetParams {
     int32_t max_segs, max_slots;
     // workspace
     struct RetSeg* segs;
-    int32_t* num_segs;
+    int32_t* num_segs;         // segments; whether a request has no slot
     float* seg_decay;          // [slots][H]
     float* slots;              // [slots][H][D][D]
 };
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(256) retention_step(const RetParams p) {
 // ------------------------------------------------------------------ segments
 
 // Time of both chunk passes, in eighths of a chunk with outputs, if requests are cut into
-// `segs` segments of up to `chunks` chunks (`cut` of them not a request's last, `all` chunks
+// `segs` segments of up to `chunks` chunks (`cut` of them of requests of several, `all` chunks
 // together) over `units` heads and slices: rounds of whole segments on all SMs, or the work
 // evenly spread and one segment more, whichever is less. A segment costs about 4 chunks
 // beside its own; a chunk without outputs half of one with.
@@ -208,10 +208,11 @@ __device__ __forceinline__ int64_t pass_time(int64_t segs, int64_t cut, int64_t 
 // One CTA: segments of every request of two tokens or more, in request order. Their length
 // is the best of 32, from the shortest that the workspace has room for upwards.
 __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t units, int32_t sms) {
-    __shared__ int32_t tot[2][32];
+    __shared__ int32_t tot[3][32], need[32];
     __shared__ int64_t cost[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int64_t single0 = p.max_slots;  // slots that requests of one segment may take
     if (p.max_slots > 0 && p.num_reqs <= kChooseReqs) {
         const float grown = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(warp) / 6.f);
         const int32_t seg = min((static_cast<int32_t>(fminf(grown, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
@@ -222,8 +223,8 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
             if (!ret_request(p, r, false, q0, q1, where, fresh) || q1 - q0 < 2) continue;
             const int32_t n = (q1 - q0 + seg - 1) / seg;
             segs += n;
-            if (n > 1) slots += n;
-            cut += n - 1;
+            if (n > 1) slots += n + 1;
+            if (n > 1) cut += n;
             all += (q1 - q0 + kChunk - 1) / kChunk;
             longest = max(longest, min(q1 - q0, seg));
         }
@@ -232,6 +233,7 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
         cut = __reduce_add_sync(0xffffffffu, cut);
         all = __reduce_add_sync(0xffffffffu, all);
         longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 0) need[warp] = slots;
         if (lane == 0)
             cost[warp] = segs > p.max_segs || slots > p.max_slots
                              ? INT64_MAX
@@ -242,61 +244,78 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
             if (cost[i] < cost[best]) best = i;
         const float chosen = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(best) / 6.f);
         p.seg_tokens = min((static_cast<int32_t>(fminf(chosen, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
+        single0 = need[best];
     }
     int64_t seg0 = 0, slot0 = 0;
+    int32_t finals = 0;
     for (int32_t base = 0; base < p.num_reqs; base += 1024) {
         const int32_t r = base + tid;
         int32_t q0 = 0, q1 = 0, where, n = 0;
         bool fresh;
         if (r < p.num_reqs && ret_request(p, r, false, q0, q1, where, fresh) && q1 - q0 > 1)
             n = (q1 - q0 + p.seg_tokens - 1) / p.seg_tokens;
-        const int32_t m = n > 1 ? n : 0;
-        int32_t a = n, b = m;  // inclusive sums over the warp
+        // slots: before each segment and after the last; for one segment of some length too,
+        // as far as there is room, so that its state is worked out beside the others'
+        const int32_t m = n > 1 ? n + 1 : 0, k = n == 1 && q1 - q0 > 2 * kChunk ? 2 : 0;
+        int32_t a = n, b = m, d = k;  // inclusive sums over the warp
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int32_t x = __shfl_up_sync(0xffffffffu, a, off), y = __shfl_up_sync(0xffffffffu, b, off);
+            const int32_t z = __shfl_up_sync(0xffffffffu, d, off);
             if (lane >= off) {
                 a += x;
                 b += y;
+                d += z;
             }
         }
         if (lane == 31) {
             tot[0][warp] = a;
             tot[1][warp] = b;
+            tot[2][warp] = d;
         }
         __syncthreads();
-        int64_t first = seg0 + a - n, slot = slot0 + b - m;
+        int64_t first = seg0 + a - n, slot = slot0 + b - m, single = single0 + d - k;
         for (int w = 0; w < 32; ++w) {
             if (w < warp) {
                 first += tot[0][w];
                 slot += tot[1][w];
+                single += tot[2][w];
             }
             seg0 += tot[0][w];
             slot0 += tot[1][w];
+            single0 += tot[2][w];
         }
         // Offsets that run backwards can claim more than the workspace holds: a request
         // that does not fit is listed with no segment (count 0).
         const bool fits = first + n <= p.max_segs && slot + m <= p.max_slots;
         if (n > 0 && !fits) set_err(p.err, YOCO_DEVERR_OFFSETS);
+        const bool slotted = m > 0 || (k > 0 && single + k <= p.max_slots);
+        const int32_t at = static_cast<int32_t>(m ? slot : single);
+        if (n > 0 && fits && !slotted) ++finals;
         for (int32_t i = 0; i < n && first + i < p.max_segs; ++i) {
             RetSeg s;
             s.req = r;
             s.token = q0 + i * p.seg_tokens;
             s.tokens = min(p.seg_tokens, q1 - s.token);
-            s.slot = m ? static_cast<int32_t>(slot) + i : -1;
+            s.slot = slotted ? at + i : -1;
             s.index = i;
             s.count = fits ? n : 0;
-            s.base = static_cast<int32_t>(slot);
+            s.base = at;
             s.pad = 0;
             p.segs[first + i] = s;
         }
         __syncthreads();
     }
-    if (tid == 0) *p.num_segs = static_cast<int32_t>(seg0 < p.max_segs ? seg0 : p.max_segs);
+    finals = __syncthreads_count(finals > 0);
+    if (tid == 0) {
+        p.num_segs[0] = static_cast<int32_t>(seg0 < p.max_segs ? seg0 : p.max_segs);
+        p.num_segs[1] = finals;
+    }
 }
 
-// State before each segment of a request: slot 0 is its own state (or zero),
-// slot i + 1 = decay of segment i * slot i + what segment i adds.
+// State before each segment of a request with slots: slot 0 gets its own state (or zero), slot i + 1
+// the decay of segment i * slot i + what segment i adds, which it holds; the last of them is
+// the state after the request.
 template <int D>
 __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
     constexpr int PARTS = D * D / 1024;  // CTAs of a (request, head)
@@ -304,38 +323,37 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
     const int32_t n = *p.num_segs;
     for (int64_t item = blockIdx.x; item < static_cast<int64_t>(n) * p.H * PARTS; item += gridDim.x) {
         const RetSeg s = p.segs[item / (p.H * PARTS)];
-        if (s.count <= 1 || s.index != 0) continue;
+        if (s.count == 0 || s.index != 0 || s.slot < 0) continue;
         const int32_t h = static_cast<int32_t>(item / PARTS % p.H), part = static_cast<int32_t>(item % PARTS);
         const int64_t at = static_cast<int64_t>(part) * 1024 + threadIdx.x * 4;
+        const int64_t own = (static_cast<int64_t>(__ldg(p.where + s.req)) * p.H + h) * D * D + at;
         const int32_t q = __ldg(p.qsl + s.req + 1) - __ldg(p.qsl + s.req);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (__ldg(p.seq_lens + s.req) > q)
-            x = *reinterpret_cast<const float4*>(
-                p.state + (static_cast<int64_t>(__ldg(p.where + s.req)) * p.H + h) * D * D + at);
+        if (__ldg(p.seq_lens + s.req) > q) x = *reinterpret_cast<const float4*>(p.state + own);
         float* slot = p.slots + (static_cast<int64_t>(s.base) * p.H + h) * D * D + at;
         const int64_t stride = static_cast<int64_t>(p.H) * D * D;
-        *reinterpret_cast<float4*>(slot) = x;
         constexpr int AHEAD = 8;  // loads do not wait for the sums
-        for (int32_t i = 0; i + 1 < s.count; i += AHEAD) {
+        for (int32_t i = 0; i < s.count; i += AHEAD) {
             float4 y[AHEAD];
             float a[AHEAD];
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u)
-                if (i + u + 1 < s.count) {
+                if (i + u < s.count) {
                     y[u] = *reinterpret_cast<const float4*>(slot + (u + 1) * stride);
                     a[u] = p.seg_decay[static_cast<int64_t>(s.base + i + u) * p.H + h];
                 }
 #pragma unroll
             for (int u = 0; u < AHEAD; ++u)
-                if (i + u + 1 < s.count) {
+                if (i + u < s.count) {
+                    *reinterpret_cast<float4*>(slot + u * stride) = x;
                     x.x = fmaf(a[u], x.x, y[u].x);
                     x.y = fmaf(a[u], x.y, y[u].y);
                     x.z = fmaf(a[u], x.z, y[u].z);
                     x.w = fmaf(a[u], x.w, y[u].w);
-                    *reinterpret_cast<float4*>(slot + (u + 1) * stride) = x;
                 }
             slot += AHEAD * stride;
         }
+        *reinterpret_cast<float4*>(p.state_out + own) = x;
     }
 }
 
@@ -353,9 +371,13 @@ __global__ void __launch_bounds__(256) retention_scan(const RetParams p) {
 // q, k and v lie in shared memory as blocks of 64 elements a row with the
 // 128-byte swizzle, which serve as K-major and as MN-major operands alike: no
 // operand is transposed by a thread. Roundings to bf16: P and the state's copy,
-// both below the rounding of the output; the decayed v as a sum of three bf16
-// terms (24 bits) where the state leaves the kernel, of two (16 bits) where it
-// only feeds later outputs of its segment.
+// both below the rounding of the output; the decayed v as a sum of bf16 terms: two
+// (16 bits) for the state that feeds later outputs of its segment, three (24
+// bits) for states that leave the call, which retention_add works out apart:
+// the tensor cores cut every sum towards zero, 2^-24 of it on average, so that
+// a state added to for a whole prompt would lose some 10^-6 of itself. There
+// a chunk's products start from zero and are added to the state in fp32, to
+// nearest.
 
 constexpr int kVal = 128;                  // value dims of a CTA (head_dim 64: 64 of its rows idle)
 constexpr int kBlockBytes = kChunk * 128;  // 64 tokens x 64 elements
@@ -406,9 +428,9 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* src
 }
 
 // exp(L_end - L_j) v_j as bf16 terms, each cut from what the ones before it leave, into
-// `terms` (VB bytes each); w: the factors of the chunk's tokens.
-template <int VD, int VB, int THREADS>
-__device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, const float* w, bool three, int thread) {
+// `terms` (TERMS of VB bytes each); w: the factors of the chunk's tokens.
+template <int VD, int VB, int TERMS, int THREADS>
+__device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, const float* w, int thread) {
 #pragma unroll
     for (int x = thread; x < kChunk * (VD / 8); x += THREADS) {
         const int t = x / (VD / 8), j = x % (VD / 8);
@@ -424,7 +446,7 @@ __device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, 
             lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
             hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
             r1[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
-            if (three) {
+            if (TERMS == 3) {
                 lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
                 hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
                 r2[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
@@ -432,21 +454,22 @@ __device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, 
         }
         *reinterpret_cast<uint4*>(terms + o) = make_uint4(r0[0], r0[1], r0[2], r0[3]);
         *reinterpret_cast<uint4*>(terms + VB + o) = make_uint4(r1[0], r1[1], r1[2], r1[3]);
-        if (three) *reinterpret_cast<uint4*>(terms + 2 * VB + o) = make_uint4(r2[0], r2[1], r2[2], r2[3]);
+        if (TERMS == 3) *reinterpret_cast<uint4*>(terms + 2 * VB + o) = make_uint4(r2[0], r2[1], r2[2], r2[3]);
     }
 }
 
-// S^T += (decayed v)^T k; the issuing warp.
-template <int D>
-__device__ __forceinline__ void issue_update(uint32_t state, uint32_t terms, uint32_t k, bool three, bool add) {
+// S^T (+)= (decayed v)^T k in TERMS bf16 terms, the smallest first: the tensor cores cut each
+// sum to the accumulator's 24 bits (towards zero), which costs nothing while it is small. The
+// issuing warp.
+template <int D, int TERMS>
+__device__ __forceinline__ void issue_update(uint32_t state, uint32_t terms, uint32_t k, bool add) {
     constexpr uint32_t ID = bf16_product(128, D, true, true);
 #pragma unroll
-    for (int u = 0; u < 3; ++u)
-        if (u < 2 || three)
+    for (int u = TERMS - 1; u >= 0; --u)
 #pragma unroll
-            for (int kk = 0; kk < kChunk / 16; ++kk)
-                tmem_mma(state, smem_operand(terms + u * RetDims<D>::VB + kk * 2048, kBlockBytes, 1024),
-                         smem_operand(k + kk * 2048, kBlockBytes, 1024), ID, add || u > 0 || kk > 0);
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+            tmem_mma(state, smem_operand(terms + u * RetDims<D>::VB + kk * 2048, kBlockBytes, 1024),
+                     smem_operand(k + kk * 2048, kBlockBytes, 1024), ID, add || u < TERMS - 1 || kk > 0);
 }
 
 // Log decays of chunk c of a segment: lane l has tokens 2l and 2l + 1 (0 behind the last).
@@ -468,9 +491,10 @@ __device__ __forceinline__ void running_sums(float2 g, int lane, Sum& l0, Sum& l
     l0 = l1 + Sum{-g1.h, -g1.l};
 }
 
-// What segments add. v is decayed to the segment's end, so that S^T is only ever added to.
-// Copies run ahead (k of the next chunk, v of the one after), products behind: the terms of
-// a chunk are worked out while the products of the one before run.
+// States. Without FINAL, what each segment adds, from zero, into its slot; with FINAL, the
+// state after each request without slots (of one segment). v is decayed to the segment's end,
+// so that chunks only add up. Copies run ahead (k of the next chunk, v of the one after), and
+// the terms of a chunk are worked out while the products of the one before run.
 template <int D>
 struct RetAddShape : RetDims<D> {
     using B = RetDims<D>;
@@ -480,25 +504,28 @@ struct RetAddShape : RetDims<D> {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-template <int D>
+template <int D, bool FINAL>
 __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetParams p) {
     using S = RetAddShape<D>;
     constexpr int NS = S::NS, VD = S::VD, T = kAddThreads;
     extern __shared__ uint8_t ret_smem[];
-    __shared__ __align__(8) uint64_t bars[2];  // the products of even and odd chunks
+    __shared__ __align__(8) uint64_t bar;  // a chunk's products
     __shared__ uint32_t tmem_base;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ret_smem) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
     float* const fac = reinterpret_cast<float*>(smem + S::AT_F);
     Sum* const totals = reinterpret_cast<Sum*>(smem + S::AT_T);
+    if (FINAL) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (p.num_segs[1] == 0) return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool issuer = warp == T / 32;  // the warp that issues the products
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     if (tid == 0) {
-        mbar_init(&bars[0], 1);
-        mbar_init(&bars[1], 1);
+        mbar_init(&bar, 1);
         fence_mbar_init();
     }
     if (issuer) tmem_alloc(&tmem_base, kTensorCols);
@@ -508,19 +535,44 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base, 0);
     asm volatile("griddepcontrol.wait;" ::: "memory");               // the segments are listed
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // single tokens may run beside this
-    uint32_t ph[2] = {0, 0};
+    uint32_t ph = 0;
     bool bad = false;  // a wait has given up
-    auto wait = [&](int32_t c) {
-        const int i = c & 1;
-        if (!bad && !mbar_wait_bounded(&bars[i], i ? ph[1] : ph[0], kRetWaitNs)) bad = true;
-        if (i) ph[1] ^= 1;
-        else ph[0] ^= 1;
+    auto wait = [&]() {
+        if (!bad && !mbar_wait_bounded(&bar, ph, kRetWaitNs)) bad = true;
+        ph ^= 1;
+        tmem_fence_after();
+    };
+    // A thread's columns of its lane: a half of D, CW at a time. Products in columns 0.., the
+    // state in columns D...
+    constexpr int PARTS = T / 128, CW = D / PARTS < 32 ? D / PARTS : 32;
+    const int col0 = (warp >> 2) * (D / PARTS);
+    auto fold = [&](bool first, float* dst) {  // the state += the products; its value to dst
+        if (issuer) return;
+#pragma unroll
+        for (int b = 0; b < D / PARTS / CW; ++b) {
+            const int c0 = col0 + b * CW;
+            uint32_t x[CW], y[CW];
+            tmem_ld(tm + lanes + c0, x);
+            if (!first) tmem_ld(tm + lanes + D + c0, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
+                if (!first) x[i] = __float_as_uint(__uint_as_float(x[i]) + __uint_as_float(y[i]));
+            if (dst) {
+                if (row < VD)
+#pragma unroll
+                    for (int i = 0; i < CW; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
+            } else {
+                tmem_st(tm + lanes + D + c0, x);
+            }
+        }
+        tmem_st_wait();
     };
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
     for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const RetSeg sg = p.segs[item / (p.H * NS)];
-        if (sg.count == 0 || sg.index == sg.count - 1) continue;
+        if (sg.count == 0 || FINAL != (sg.slot < 0)) continue;
         const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
         auto load_k = [&](int32_t c) {
@@ -563,6 +615,25 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
             factors(0, chunk_decays(p, sg, h, 0, lane));
             g = chunk_decays(p, sg, h, 1, lane);
         }
+        const int64_t state_at = static_cast<int64_t>(FINAL ? __ldg(p.where + sg.req) : sg.slot + 1) * p.H + h;
+        float* const dst = (FINAL ? p.state_out : p.slots) + state_at * D * D + dv0;
+        if (FINAL && !issuer) {  // the state before the request, decayed to its end
+            Sum t = {0.f, 0.f};
+            for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
+            const float a = exp2f(warp_total(t).h);
+            const int32_t q = __ldg(p.qsl + sg.req + 1) - __ldg(p.qsl + sg.req);
+            const float* src = __ldg(p.seq_lens + sg.req) > q && row < VD ? p.state + state_at * D * D + dv0 : nullptr;
+#pragma unroll
+            for (int b = 0; b < D / PARTS / CW; ++b) {
+                const int c0 = col0 + b * CW;
+                uint32_t x[CW];
+#pragma unroll
+                for (int i = 0; i < CW; ++i)
+                    x[i] = src ? __float_as_uint(a * src[static_cast<int64_t>(c0 + i) * D + row]) : 0u;
+                tmem_st(tm + lanes + D + c0, x);
+            }
+            tmem_st_wait();
+        }
         for (int32_t c = 0; c < chunks; ++c) {
             if (c == 0) cp_async_wait<0>();
             else cp_async_wait<1>();
@@ -571,49 +642,37 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
             if (bad) break;
             const uint32_t terms = S::AT_W + (c & 1) * 3 * S::VB;
             if (!issuer) {
-                decayed_terms<VD, S::VB, T>(smem + S::AT_V + c % 3 * S::VB, smem + terms, fac + (c & 1) * kChunk, true, tid);
+                decayed_terms<VD, S::VB, 3, T>(smem + S::AT_V + c % 3 * S::VB, smem + terms, fac + (c & 1) * kChunk, tid);
             } else if (c + 1 < chunks) {
                 factors(c + 1, g);
                 g = chunk_decays(p, sg, h, c + 2, lane);
             }
             cp_async_wait<0>();  // k of chunk c
             fence_proxy_async_smem();
+            if (c > 0) {  // the chunk before: done with its k and terms
+                wait();
+                fold(!FINAL && c == 1, nullptr);
+            }
             tmem_fence_before();
             __syncthreads();
             tmem_fence_after();
             if (issuer) {
-                issue_update<D>(tm, base + terms, base + (c & 1) * S::KB, true, c > 0);
-                tmem_commit(&bars[c & 1]);
+                issue_update<D, 3>(tm, base + terms, base + (c & 1) * S::KB, false);
+                tmem_commit(&bar);
             }
-            // the products of the chunk before are done with its k and terms
-            if (c > 0) wait(c - 1);
             load_k(c + 1);
             load_v(c + 2);
             cp_async_commit();
         }
-        if (!bad) wait(chunks - 1);
+        if (!bad) wait();
         bad = __syncthreads_or(bad);
         if (bad) break;
-        tmem_fence_after();
-        float* dst = p.slots + (static_cast<int64_t>(sg.slot + 1) * p.H + h) * D * D + dv0;
-        if (!issuer) {
-            constexpr int PARTS = T / 128, CW = D / PARTS < 32 ? D / PARTS : 32;
-#pragma unroll
-            for (int b = 0; b < D / PARTS / CW; ++b) {
-                const int c0 = (warp >> 2) * (D / PARTS) + b * CW;
-                uint32_t x[CW];
-                tmem_ld(tm + lanes + c0, x);
-                tmem_ld_wait();
-                if (row < VD)
-#pragma unroll
-                    for (int i = 0; i < CW; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
-            }
-            if (dv0 == 0 && warp == 0) {  // the segment's decay
-                Sum t = {0.f, 0.f};
-                for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
-                t = warp_total(t);
-                if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(t.h);
-            }
+        fold(!FINAL && chunks == 1, dst);
+        if (!FINAL && dv0 == 0 && warp == 0) {  // the segment's decay
+            Sum t = {0.f, 0.f};
+            for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
+            t = warp_total(t);
+            if (lane == 0) p.seg_decay[static_cast<int64_t>(sg.slot) * p.H + h] = exp2f(t.h);
         }
         tmem_fence_before();
     }
@@ -637,7 +696,7 @@ template <int D>
 struct RetOutShape : RetDims<D> {
     using B = RetDims<D>;
     static constexpr int STAGE = 2 * B::KB + B::VB;  // q, k, v
-    static constexpr int AT_W = 2 * STAGE, AT_P = AT_W + 3 * B::VB, AT_F = AT_P + kBlockBytes + B::PAD;
+    static constexpr int AT_W = 2 * STAGE, AT_P = AT_W + 2 * B::VB, AT_F = AT_P + kBlockBytes + B::PAD;
     // of each of 4 chunks, for its 64 tokens t: the running sum L_t (high and low parts, log2
     // units), exp(L_t), exp(L_end - L_t), exp(L_t - L_mid), exp(L_mid - L_t)
     static constexpr int FACTORS = 6;
@@ -696,7 +755,6 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
     for (int32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const RetSeg sg = p.segs[item / (p.H * NS)];
         if (sg.count == 0) continue;
-        const bool last = sg.index == sg.count - 1;  // the state after it leaves the kernel
         const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
         // chunk c into its stage: k by the 128 loader threads, q and v by the value warps
@@ -798,7 +856,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
             const uint32_t at = (c & 1) * S::STAGE;  // of the chunk's q, k, v
             const uint32_t sq = base + at, sk = sq + S::KB, sv = sk + S::KB;
             const float* f = fac + (c & 3) * F;
-            const bool update = last || c + 1 < chunks;
+            const bool update = c + 1 < chunks;
             if (copies) {
                 cp_async_wait<0>();
                 fence_proxy_async_smem();
@@ -837,7 +895,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
                 }
                 tmem_st_wait();
             } else if (update) {
-                decayed_terms<VD, S::VB, 256>(smem + at + 2 * S::KB, smem + S::AT_W, f + 3 * kChunk, last, tid - 256);
+                decayed_terms<VD, S::VB, 2, 256>(smem + at + 2 * S::KB, smem + S::AT_W, f + 3 * kChunk, tid - 256);
                 fence_proxy_async_smem();
             }
             tmem_fence_before();
@@ -850,7 +908,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
                                 smem_operand(sq + (kk >> 2) * kBlockBytes + (kk & 3) * 32, 16, 1024),
                                 bf16_product(128, kChunk, false, false), kk > 0);
                 if (update) {
-                    issue_update<D>(tm + S::TS, base + S::AT_W, sk, last, true);
+                    issue_update<D, 2>(tm + S::TS, base + S::AT_W, sk, true);
                     tmem_commit(&bar_s);
                 }
             } else if (!of_state) {
@@ -919,7 +977,6 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
             }
         }
         if (!bad) {
-            if (of_state && pending) wait(&bar_s, ph_s);
             if (!of_state && !issuer) {
                 take_outputs(chunks - 1);
                 write_outputs(chunks - 1);
@@ -928,19 +985,6 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
         bad = __syncthreads_or(bad);
         if (bad) break;
         tmem_fence_after();
-        if (last && of_state) {  // the state after the request
-            float* dst = p.state_out + (static_cast<int64_t>(__ldg(p.where + sg.req)) * p.H + h) * D * D + dv0;
-#pragma unroll
-            for (int b = 0; b < D / 2 / CW; ++b) {
-                const int c0 = half * (D / 2) + b * CW;
-                uint32_t x[CW];
-                tmem_ld(tm + lanes + S::TS + c0, x);
-                tmem_ld_wait();
-                if (row < VD)
-#pragma unroll
-                    for (int i = 0; i < CW; ++i) dst[static_cast<int64_t>(c0 + i) * D + row] = __uint_as_float(x[i]);
-            }
-        }
         tmem_fence_before();
     }
     cp_async_wait<0>();
@@ -980,7 +1024,7 @@ RetPlan ret_plan(int64_t R, int64_t T, int64_t max_q, int H, int D) {
     const int64_t shorter = R < T / 2 ? R : T / 2;
     const int64_t cut = max_q > seg ? T / seg : 0;
     x.max_segs = T / seg + shorter;
-    x.max_slots = 2 * cut;
+    x.max_slots = 3 * cut;  // at most n + 1 for a request of n > 1 segments, n / 2 of them whole
     return x;
 }
 
@@ -991,7 +1035,7 @@ RetPlan ret_sizes(int64_t R, int64_t T, int64_t max_q, int H, int D) {
     int64_t whole = ret_target(H, D);
     if (whole < T / kMaxSegment) whole = T / kMaxSegment;
     if (whole > T / kMinSegment) whole = T / kMinSegment;
-    const int64_t segs = whole + (R < T / 2 ? R : T / 2), slots = max_q > kMinSegment ? 2 * whole : 0;
+    const int64_t segs = whole + (R < T / 2 ? R : T / 2), slots = max_q > kMinSegment ? 3 * whole : 0;
     x.list_bytes = (16 + static_cast<size_t>(segs) * sizeof(RetSeg) + 255) & ~static_cast<size_t>(255);
     x.decay_bytes = (static_cast<size_t>(slots) * H * 4 + 255) & ~static_cast<size_t>(255);
     x.bytes = x.list_bytes + x.decay_bytes + static_cast<size_t>(slots) * H * D * D * 4;
@@ -1020,9 +1064,10 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
         e = cudaGetLastError();
         if (e != cudaSuccess || p.seg_tokens == 0) return e;
     }
-    static unsigned long long done_out = 0, done_add = 0;
+    static unsigned long long done_out = 0, done_add = 0, done_final = 0;
     e = ret_smem_attr(retention_out<D>, RetOutShape<D>::SMEM, done_out);
-    if (e == cudaSuccess) e = ret_smem_attr(retention_add<D>, RetAddShape<D>::SMEM, done_add);
+    if (e == cudaSuccess) e = ret_smem_attr(retention_add<D, false>, RetAddShape<D>::SMEM, done_add);
+    if (e == cudaSuccess) e = ret_smem_attr(retention_add<D, true>, RetAddShape<D>::SMEM, done_final);
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count(), units = p.H * RetDims<D>::NS;
     const int64_t items = static_cast<int64_t>(p.max_segs) * units;
@@ -1043,7 +1088,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(kAddThreads + 32);
         cfg.dynamicSmemBytes = RetAddShape<D>::SMEM;
-        e = cudaLaunchKernelEx(&cfg, retention_add<D>, p);
+        e = cudaLaunchKernelEx(&cfg, retention_add<D, false>, p);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(steps);
         cfg.blockDim = dim3(256);
@@ -1058,7 +1103,13 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kOutThreads + 32);
     cfg.dynamicSmemBytes = RetOutShape<D>::SMEM;
-    return cudaLaunchKernelEx(&cfg, retention_out<D>, p);
+    e = cudaLaunchKernelEx(&cfg, retention_out<D>, p);
+    if (e != cudaSuccess) return e;
+    // requests without slots: their states may lie in the place of those that the outputs
+    // start from, so they are written last
+    cfg.blockDim = dim3(kAddThreads + 32);
+    cfg.dynamicSmemBytes = RetAddShape<D>::SMEM;
+    return cudaLaunchKernelEx(&cfg, retention_add<D, true>, p);
 }
 
 bool ret_shape_ok(int32_t H, int32_t D) {
