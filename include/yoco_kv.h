@@ -461,7 +461,8 @@ yoco_status_t yoco_cross_attn_paged_e2m1(const void* q, const void* k_cache, con
  * they continue the state of the tokens before them, or start from zero when
  * seq_lens[r] equals their number (that state is then not read).
  *   q, out         device bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned; rows from
- *                  query_start_loc[num_reqs] on are neither read nor written
+ *                  query_start_loc[num_reqs] on are neither read nor written. out overlaps
+ *                  none of the inputs
  *   k, v           device bf16 [num_tokens][num_kv_heads][head_dim], 16-byte aligned; head h
  *                  reads k/v head h / (num_q_heads / num_kv_heads)
  *   log_decay      device float32 g, [num_tokens][num_q_heads] with decay_per_token, else
@@ -482,7 +483,9 @@ yoco_status_t yoco_cross_attn_paged_e2m1(const void* q, const void* k_cache, con
  * and its state are left as they were. head_dim 64, 128 or 256. The state and
  * every sum are fp32; outputs of prompts round the weights of a chunk and the
  * state's copy that multiplies q to bf16; the state after the step takes the
- * decayed values in 24 bits. Results do not depend on timing.
+ * decayed values in 24 bits. Prompts are worked out in chunks of 64 tokens from
+ * their first: a value that is not finite can reach the outputs of its whole
+ * chunk, the earlier tokens' too. Results do not depend on timing.
  */
 yoco_status_t yoco_retention(const void* q, const void* k, const void* v, const float* log_decay,
                              int32_t decay_per_token, const float* state, float* state_out,

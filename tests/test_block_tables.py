@@ -134,6 +134,17 @@ def test_without_a_stack_and_in_a_graph():
 
 
 @pytest.mark.gpu
+def test_an_empty_stack_is_a_stack():
+    """Free pages of length zero: requests that need one get none, whatever the table holds."""
+    from yoco_shared_kv_gb300 import _native as N
+    dev = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")  # noqa: E731
+    table, slots, after, err = dev([[3, 4], [5, 6]]), dev([9] * 3), dev([7]), dev([0])
+    N.yoco_build_block_tables(table, dev([17, 10]), dev([0, 1, 3]), 8, 16, slots, dev([]), dev([0]), after, err)
+    assert slots.tolist() == [-1, 5 * 16 + 8, 5 * 16 + 9] and int(after) == 0
+    assert int(err) == N.DEVERR_NO_PAGES and table.tolist() == [[3, 4], [5, 6]]
+
+
+@pytest.mark.gpu
 def test_empty_step():
     from yoco_shared_kv_gb300 import _native as N
     z = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731

@@ -234,6 +234,7 @@ def test_attention_of_wide_ranges(D, bs, H_q):
     q[:, :, :2] = 0
     q[1] = 0                                   # a row of zeros: the mean of V
     attend(c, q, seq, np.arange(4), scale=1e-7)
+    attend(c, queries(10, 3, H_q, D, 2.0 ** -100), seq, np.arange(4), scale=1e-30)  # scores vanish: the mean again
 
 
 @pytest.mark.gpu

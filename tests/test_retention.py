@@ -262,7 +262,7 @@ def test_refusals():
     from yoco_shared_kv_gb300 import _native as N
     L, fake = N.lib, 1 << 20
 
-    def call(q=fake, k=fake, v=fake, g=fake, s=fake, so=fake, w=fake, o=fake, qsl=fake, seq=fake, R=2, T=300, mq=290,
+    def call(q=fake, k=fake, v=fake, g=fake, s=fake, so=fake, w=fake, o=2 * fake, qsl=fake, seq=fake, R=2, T=300, mq=290,
              ns=4, H=4, Hk=2, D=128, ws=fake, ws_bytes=1 << 40, scale=1.0):
         return L.yoco_retention(q, k, v, g, 1, s, so, w, o, qsl, seq, R, T, mq, ns, H, Hk, D, ctypes.c_float(scale), ws,
                                 ws_bytes, None, None)
@@ -271,7 +271,7 @@ def test_refusals():
     assert call(H=1 << 20, Hk=1) == N.YOCO_ERR_UNSUPPORTED
     for bad in (dict(R=-1), dict(T=-1), dict(mq=0), dict(ns=0), dict(scale=float("nan")), dict(q=None), dict(k=None),
                 dict(v=None), dict(g=None), dict(s=None), dict(so=None), dict(w=None), dict(o=None), dict(qsl=None),
-                dict(seq=None), dict(q=fake + 2), dict(s=fake + 4), dict(ws=fake + 8)):
+                dict(seq=None), dict(q=fake + 2), dict(s=fake + 4), dict(ws=fake + 8), dict(q=fake, o=fake)):
         assert call(**bad) == N.YOCO_ERR_INVALID_ARG, bad
     assert call(ws=None) == N.YOCO_ERR_WORKSPACE
     assert call(ws_bytes=N.yoco_retention_workspace_size(2, 300, 290, 4, 128) - 1) == N.YOCO_ERR_WORKSPACE

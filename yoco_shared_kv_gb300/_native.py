@@ -433,10 +433,13 @@ def yoco_build_block_tables(block_table: torch.Tensor, seq_lens: torch.Tensor,
     R, max_blocks = block_table.shape
     T = slot_mapping.numel()
     cap = 0 if free_pages is None else free_pages.numel()
+    free = _arg(free_pages, i32, (cap,), "free_pages", dev)
+    if cap == 0 and free_pages is not None and num_free is not None:
+        free = num_free.data_ptr()  # an empty stack has no address of its own: never read
     _check("yoco_build_block_tables", lib.yoco_build_block_tables(
         _arg(block_table, i32, (R, max_blocks), "block_table", dev), max_blocks,
         _arg(seq_lens, i32, (R,), "seq_lens", dev), _arg(query_start_loc, i32, (R + 1,), "query_start_loc", dev),
-        R, T, int(num_blocks), int(block_size), _arg(free_pages, i32, (cap,), "free_pages", dev), cap,
+        R, T, int(num_blocks), int(block_size), free, cap,
         _arg(num_free, i32, (1,), "num_free", dev), _arg(num_free_after, i32, (1,), "num_free_after", dev),
         _arg(slot_mapping, i32, (T,), "slot_mapping", dev), _arg(err_word, i32, (1,), "err_word", dev),
         strm))

@@ -1239,12 +1239,15 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
                     mx = max(mx & 0xffffu, mx >> 16);
                     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const uint32_t f = max(mx >> 7, 20u);  // exponent field of the largest
+                    // exponent field of the largest (any for a row of zeros)
+                    const uint32_t f = mx == 0u ? 127u : max(mx >> 7, 20u);
                     const float up = __uint_as_float((268u - f) << 23);
                     const float down = __uint_as_float((f - 14u) << 23);
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        qscale[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, down, (2 * tq + e) * 4);
+                        // (never 0: a masked score of -inf times it must stay -inf)
+                        qscale[nt][e] = fmaxf(p.scale_log2 * __shfl_sync(0xffffffffu, down, (2 * tq + e) * 4),
+                                              1.2e-38f);
                     auto w = [up](uint32_t x) {
                         return pack_f16x2(bf16lo_to_f32(x) * up, bf16hi_to_f32(x) * up);
                     };

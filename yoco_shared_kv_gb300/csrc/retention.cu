@@ -1143,6 +1143,7 @@ extern "C" yoco_status_t yoco_retention(
         return YOCO_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(state_out) || !aligned16(out))
         return YOCO_ERR_INVALID_ARG;
+    if (out == q || out == k || out == v) return YOCO_ERR_INVALID_ARG;  // read while it is written
     // one CTA per (request, head, slice)
     if (static_cast<int64_t>(num_reqs) * num_q_heads * (head_dim / kSlice) > 0x7fffffffll) return YOCO_ERR_UNSUPPORTED;
     const int32_t longest = max_q_len < num_tokens ? max_q_len : num_tokens;
