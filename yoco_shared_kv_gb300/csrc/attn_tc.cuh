@@ -796,6 +796,93 @@ __device__ __forceinline__ void cross_cta_merge(const AttnParams& p, const TcWs&
     }
 }
 
+// The combine of a CTA's pieces for e2m1 pages walked by single warps, which
+// leave up to 32 pieces. One warp per (head, 128-element part): its lanes lie
+// side by side over the pieces first - one load of every header and statistic,
+// butterfly trees of fixed order for the maximum and the sum - and then over
+// the part, the pieces' values loaded independently of one another. The loops
+// in the kernel are a serial chain of loads per piece: 5 us of a call over 4
+// sequences of 131072 tokens. us a call, loops -> this: 39.4 -> 37.5 there,
+// 49.0 -> 47.7 for 64 decoding requests (D 256, 16-token blocks), 35.6 -> 32.2
+// at D 128. Warp pairs leave 8 pieces at most and keep the loops: 114 against
+// 120 for 64 requests of 4 rows. A call of its own, so that it takes no
+// registers from the streaming loop (inlined it spilled there).
+template <int D, int NW, int MAXE, bool RG>
+__device__ __noinline__ void f4_combine(const AttnParams& p, const TcWs& ws, const PieceHdr* hdr, int warp,
+                                        int lane, int64_t cta_lo, int64_t cta_hi) {
+    __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(p.out);
+    const int VS = p.vhs;  // virtual heads per partial slot
+    static_assert(MAXE <= 32, "one lane per piece");
+    const PieceHdr& X = hdr[lane < MAXE ? lane : 0];
+    const bool valid = lane < MAXE && X.valid;
+    const int64_t xs0 = valid ? X.s0 : -1;
+    const float* const xo = X.o;
+    const float2* const xml = X.ml;
+    uint32_t left = __ballot_sync(0xffffffffu, valid);
+#pragma unroll 1
+    while (left) {
+        const int e0 = __ffs(left) - 1;
+        const int64_t s0 = __shfl_sync(0xffffffffu, xs0, e0);
+        const uint32_t mine = __ballot_sync(0xffffffffu, valid && xs0 == s0);
+        left &= ~mine;
+        const PieceHdr& H = hdr[e0];
+        const int32_t gn = H.n, gg = H.g;
+        const bool whole = s0 >= cta_lo && H.s1 <= cta_hi;
+        const int items = (RG ? H.nr : 1) * p.G * (D / 128);
+#pragma unroll 1
+        for (int it = warp; it < items; it += NW) {
+            const int h = it / (D / 128), d0 = (it % (D / 128)) * 128 + lane * 4;
+            const bool in = mine >> lane & 1u;
+            const float2 ml = in ? xml[h] : make_float2(-INFINITY, 0.f);
+            float M = ml.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            const float f = ml.x != -INFINITY ? exp2_approx(ml.x - M) : 0.f;
+            float L = ml.y * f;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            uint32_t todo = mine;
+#pragma unroll 1
+            while (todo) {  // four entries a step
+                float4 x[4];
+                float fe[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = todo ? __ffs(todo) - 1 : e0;
+                    const float g = __shfl_sync(0xffffffffu, f, e);
+                    const float* const xe = reinterpret_cast<const float*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(xo), e));
+                    fe[u] = todo ? g : 0.f;
+                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (todo) x[u] = *reinterpret_cast<const float4*>(xe + h * D + d0);
+                    todo &= todo - 1;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    O.x += x[u].x * fe[u];
+                    O.y += x[u].y * fe[u];
+                    O.z += x[u].z * fe[u];
+                    O.w += x[u].w * fe[u];
+                }
+            }
+            if (whole) {
+                if (RG && L == 0.f) continue;  // a group row without keys: zero-filled above
+                const float inv = 1.f / L;
+                const int hr = RG ? h / p.G : 0;
+                __nv_bfloat162* const dst = reinterpret_cast<__nv_bfloat162*>(
+                    outp + ((static_cast<int64_t>(gn) + hr) * p.H_q + gg * p.G + (h - hr * p.G)) * D + d0);
+                dst[0] = __floats2bfloat162_rn(O.x * inv, O.y * inv);
+                dst[1] = __floats2bfloat162_rn(O.z * inv, O.w * inv);
+            } else {
+                const int64_t cp = (static_cast<int64_t>(blockIdx.x) * 2 + (s0 < cta_lo ? 0 : 1)) * VS + h;
+                *reinterpret_cast<float4*>(ws.c_o + cp * D + d0) = O;
+                if (d0 == 0) ws.c_ml[cp] = make_float2(M, L);
+            }
+        }
+    }
+}
+
 // --------------------------------------------------------------- kernel
 
 // FUSE: fused decode step (append this step's tokens, patch them into the
@@ -2068,7 +2155,8 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     // segment's heads: idle)
     const int tph = static_cast<int>(blockDim.x) / (RG ? VS : p.G);
     const int ch = static_cast<int>(threadIdx.x) / tph;
-    int e0 = 0;
+    if constexpr (F4 && !PR) f4_combine<D, NW, MAXE, RG>(p, ws, &hdr[0][0], warp, lane, cta_lo, cta_hi);
+    int e0 = F4 && !PR ? MAXE : 0;
     for (;;) {
         while (e0 < MAXE && !hdr[e0 >> 1][e0 & 1].valid) ++e0;
         if (e0 >= MAXE || (NTG != 1 && !RG && ch >= p.G)) break;
