@@ -190,26 +190,24 @@ __global__ void __launch_bounds__(256) retention_step(const RetParams p) {
 
 // ------------------------------------------------------------------ segments
 
-// Time of both chunk passes, in eighths of a chunk with outputs, if requests are cut into
-// `segs` segments of up to `chunks` chunks (`cut` of them of requests of several, `all` chunks
-// together) over `units` heads and slices: rounds of whole segments on all SMs, or the work
-// evenly spread and one segment more, whichever is less. A segment costs about 4 chunks
-// beside its own; a chunk without outputs half of one with.
-__device__ __forceinline__ int64_t pass_time(int64_t segs, int64_t cut, int64_t all, int64_t chunks,
-                                             int64_t units, int64_t sms) {
-    auto one = [&](int64_t n, int64_t work) {
-        const int64_t rounds = (n * units + sms - 1) / sms * (chunks + 4);
-        const int64_t even = (work + 4 * n) * units / sms + chunks + 4;
-        return rounds < even ? rounds : even;
-    };
-    return 8 * one(segs, all) + (cut ? 4 * one(cut, cut * chunks) : 0);
+// Time of both chunk passes, in chunks with outputs, if requests are cut into `segs` segments
+// of up to `chunks` chunks (`cut` of them of requests of several, `all` chunks together) over
+// `units` heads and slices: rounds of whole segments on all SMs, or the work evenly spread and
+// one segment more, whichever is less. A segment costs about 4 chunks beside its own; a chunk
+// without outputs two thirds of one with.
+__device__ __forceinline__ float pass_time(int32_t segs, int32_t cut, int32_t all, int32_t chunks, int32_t units,
+                                           int32_t sms) {
+    const float per = static_cast<float>(units) / static_cast<float>(sms), own = static_cast<float>(chunks + 4);
+    auto one = [&](float n, float work) { return fminf(ceilf(n * per) * own, (work + 4.f * n) * per + own); };
+    const float n = static_cast<float>(segs), m = static_cast<float>(cut);
+    return one(n, static_cast<float>(all)) + (cut ? 0.67f * one(m, m * static_cast<float>(chunks)) : 0.f);
 }
 
 // One CTA: segments of every request of two tokens or more, in request order. Their length
 // is the best of 32, from the shortest that the workspace has room for upwards.
 __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t units, int32_t sms) {
     __shared__ int32_t tot[3][32], need[32];
-    __shared__ int64_t cost[32];
+    __shared__ float cost[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int64_t single0 = p.max_slots;  // slots that requests of one segment may take
@@ -236,12 +234,12 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
         if (lane == 0) need[warp] = slots;
         if (lane == 0)
             cost[warp] = segs > p.max_segs || slots > p.max_slots
-                             ? INT64_MAX
+                             ? INFINITY
                              : pass_time(segs, cut, all, (longest + kChunk - 1) / kChunk, units, sms);
         __syncthreads();
-        int best = 0;
-        for (int i = 1; i < 32; ++i)
-            if (cost[i] < cost[best]) best = i;
+        const uint32_t mine = __float_as_uint(cost[lane]);  // not negative: its bits are in order
+        const uint32_t least = __reduce_min_sync(0xffffffffu, mine);
+        const int best = __ffs(__ballot_sync(0xffffffffu, mine == least)) - 1;
         const float chosen = static_cast<float>(p.seg_tokens) * exp2f(static_cast<float>(best) / 6.f);
         p.seg_tokens = min((static_cast<int32_t>(fminf(chosen, 1e6f)) + kChunk - 1) / kChunk * kChunk, kMaxSegment);
         single0 = need[best];
@@ -275,16 +273,20 @@ __global__ void __launch_bounds__(1024) retention_plan(RetParams p, int32_t unit
         }
         __syncthreads();
         int64_t first = seg0 + a - n, slot = slot0 + b - m, single = single0 + d - k;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) {
-                first += tot[0][w];
-                slot += tot[1][w];
-                single += tot[2][w];
+        auto over_warps = [&](int i, int64_t& before, int64_t& all) {  // the warps' sums
+            int64_t v = tot[i][lane];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, v, off);
+                if (lane >= off) v += x;
             }
-            seg0 += tot[0][w];
-            slot0 += tot[1][w];
-            single0 += tot[2][w];
-        }
+            const int64_t x = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+            if (warp > 0) before += x;
+            all += __shfl_sync(0xffffffffu, v, 31);
+        };
+        over_warps(0, first, seg0);
+        over_warps(1, slot, slot0);
+        over_warps(2, single, single0);
         // Offsets that run backwards can claim more than the workspace holds: a request
         // that does not fit is listed with no segment (count 0).
         const bool fits = first + n <= p.max_segs && slot + m <= p.max_slots;
