@@ -143,12 +143,12 @@ __global__ void __launch_bounds__(kTableThreads)
     // the requests that end at or before this CTA's first token: how many, and their demand
     int64_t before = 0;
     int32_t count = 0;
-    for (int32_t base = 0; base < num_reqs; base += kTableThreads) {
-        const int32_t r = base + tid;
-        if (r < num_reqs && __ldg(qsl + r + 1) <= t0) {
+#pragma unroll 4
+    for (int32_t r = tid; r < num_reqs; r += kTableThreads) {
+        const Request x = load_request(qsl, seq_lens, r, num_tokens, bshift, max_blocks, take);
+        if (x.q1 <= t0) {
             ++count;
-            if (take)
-                before += load_request(qsl, seq_lens, r, num_tokens, bshift, max_blocks, take).take;
+            before += x.take;
         }
     }
     int64_t r_first;

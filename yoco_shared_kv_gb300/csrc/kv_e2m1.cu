@@ -23,14 +23,17 @@ namespace {
 
 constexpr int kRowWarps = 8;
 
-// Largest finite bf16 magnitude of eight (packed pairs), infinities and NaN
-// counted as the largest finite value, as a bf16 bit pattern.
-__device__ __forceinline__ uint32_t absmax8(uint4 a) {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight bf16 values with infinities and NaN as the largest finite value of
+// their sign; returns the largest magnitude, as a bf16 bit pattern.
+__device__ __forceinline__ uint32_t finite8(uint4& a) {
+    uint32_t* w = &a.x;
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-    m = __vminu2(m, 0x7f7f7f7fu);
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mag = __vminu2(w[i] & 0x7fff7fffu, 0x7f7f7f7fu);
+        m = __vmaxu2(m, mag);
+        w[i] = mag | (w[i] & 0x80008000u);
+    }
     return max(m & 0xffffu, m >> 16);
 }
 
@@ -50,27 +53,19 @@ __device__ __forceinline__ uint32_t e2m1x2_rn_sat(float lo, float hi) {
     return r;
 }
 
-// A NaN keeps its sign and becomes the largest finite value, as an infinity does.
-__device__ __forceinline__ float finite_of(uint32_t bits) {
-    const float x = __uint_as_float(bits);
-    return x != x ? __uint_as_float((bits & 0x80000000u) | 0x7f7f0000u) : x;
-}
-
-// Eight bf16 values -> eight codes of value * inv (inv the power of two 1 / scale).
+// Eight finite bf16 values -> eight codes of value * inv (inv the power of two 1 / scale).
 __device__ __forceinline__ uint32_t quantise8_e2m1(uint4 a, float inv) {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-    uint32_t r = 0;
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r |= e2m1x2_rn_sat(finite_of(w[i] << 16) * inv, finite_of(w[i] & 0xffff0000u) * inv)
-             << (8 * i);
-    return r;
+    for (int i = 0; i < 4; ++i) c[i] = e2m1x2_rn_sat(bf16lo_to_f32(w[i]) * inv, bf16hi_to_f32(w[i]) * inv);
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
 }
 
 // Codes and scale byte of this lane's eight elements; the four lanes of a
 // block (lane & ~3) agree on the byte. All lanes of the warp take part.
 __device__ __forceinline__ void encode8(uint4 a, uint32_t& codes, int32_t& b) {
-    uint32_t m = absmax8(a);
+    uint32_t m = finite8(a);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     b = scale_byte(m);
