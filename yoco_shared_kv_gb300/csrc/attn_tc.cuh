@@ -642,7 +642,7 @@ __host__ __device__ __forceinline__ int merge_scratch_floats(int ctas, int G, in
     return (G * D + 10 * ctas + 14 * (G + 1) + 4 + 3) & ~3;
 }
 
-template <int D, bool RG>
+template <int D, bool RG, bool VEC>
 __device__ __forceinline__ void cross_cta_merge(const AttnParams& p, const TcWs& ws,
                                                 const CtaHdr& Hc, float* scratch) {
     const int32_t c = blockIdx.x, ctas = gridDim.x;
@@ -765,6 +765,42 @@ __device__ __forceinline__ void cross_cta_merge(const AttnParams& p, const TcWs&
     }
     __syncthreads();
     __nv_bfloat16* outp = static_cast<__nv_bfloat16*>(p.out);
+    if constexpr (VEC) {
+        // the same sums, four outputs (of one head: shares are whole vectors) a
+        // step: with groups of rows a half has 2048 of them, 10500 clocks one by
+        // one. us a call, 64 requests of 4 rows: 114.1 -> 110.9
+#pragma unroll 1
+        for (int e = 4 * tl; e < nout; e += 4 * half) {
+            const int v = (lo + e) / D, hh = v - h_lo, d = lo + e - v * D;
+            float4 a[4] = {};
+            auto add = [&](float4& x, int j) {
+                const float f = sf[j * nhd + hh];
+                if (f == 0.f) return;  // a holder with no key: its slot was never written
+                const float4 y = *reinterpret_cast<const float4*>(so + j * nout + e);
+                x.x += y.x * f;
+                x.y += y.y * f;
+                x.z += y.z * f;
+                x.w += y.w * f;
+            };
+            int j = 0;
+#pragma unroll 1
+            for (; j + 4 <= nh_; j += 4)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) add(a[u], j + u);
+#pragma unroll 1
+            for (; j < nh_; ++j) add(a[0], j);
+            const float inv = sInvL[hh];
+            if (RG && !(inv < INFINITY)) continue;  // a group row without keys: zero-filled in the kernel
+            const int hr = RG ? v / G : 0;  // virtual head v = (row of the group) * G + head
+            __nv_bfloat162* const dst = reinterpret_cast<__nv_bfloat162*>(
+                outp + ((static_cast<int64_t>(sg.n) + hr) * p.H_q + sg.g * G + (v - hr * G)) * D + d);
+            dst[0] = __floats2bfloat162_rn(((a[0].x + a[1].x) + (a[2].x + a[3].x)) * inv,
+                                           ((a[0].y + a[1].y) + (a[2].y + a[3].y)) * inv);
+            dst[1] = __floats2bfloat162_rn(((a[0].z + a[1].z) + (a[2].z + a[3].z)) * inv,
+                                           ((a[0].w + a[1].w) + (a[2].w + a[3].w)) * inv);
+        }
+        return;
+    }
     // a holder with no key has f = 0 and a slot never written: select, not 0 * x
     auto term = [&](int j, int e, int hh) {
         const float f = sf[j * nhd + hh];
@@ -2273,7 +2309,7 @@ __global__ void __launch_bounds__(TcShape<D, BS, FMT, NT, PR>::NW * 32, 1)
     // can only take an SM as this grid's CTAs exit, and it waits for the whole
     // grid before it touches the workspace, queries or outputs.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    cross_cta_merge<D, RG>(p, ws, cta_hdr, reinterpret_cast<float*>(smem));
+    cross_cta_merge<D, RG, F4>(p, ws, cta_hdr, reinterpret_cast<float*>(smem));
 }
 
 // One-time (per device) setting of a kernel's dynamic shared memory limit.
