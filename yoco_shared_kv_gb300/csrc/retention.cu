@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kChunk = 64;         // tokens of a chunk
 constexpr int kSlice = 64;         // value dims of a single token's CTA
-constexpr int kAddThreads = 256;   // and one warp that issues the products
+constexpr int kAddThreads = 256;   // and a warp that issues the products, and one for the factors
 constexpr int kOutThreads = 512;   // likewise
 constexpr uint64_t kRetWaitNs = 1000000000ull;  // before a wait gives up
 constexpr int kMaxChunks = 512;                 // of a segment
@@ -507,7 +507,7 @@ struct RetAddShape : RetDims<D> {
 };
 
 template <int D, bool FINAL>
-__global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetParams p) {
+__global__ void __launch_bounds__(kAddThreads + 64, 1) retention_add(const RetParams p) {
     using S = RetAddShape<D>;
     constexpr int NS = S::NS, VD = S::VD, T = kAddThreads;
     extern __shared__ uint8_t ret_smem[];
@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool issuer = warp == T / 32;  // the warp that issues the products
+    const bool decays = warp > T / 32;   // the warp that works out the factors
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     if (tid == 0) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
     constexpr int PARTS = T / 128, CW = D / PARTS < 32 ? D / PARTS : 32;
     const int col0 = (warp >> 2) * (D / PARTS);
     auto fold = [&](bool first, float* dst) {  // the state += the products; its value to dst
-        if (issuer) return;
+        if (warp >= T / 32) return;
 #pragma unroll
         for (int b = 0; b < D / PARTS / CW; ++b) {
             const int c0 = col0 + b * CW;
@@ -578,13 +579,13 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
         const int32_t h = item / NS % p.H, dv0 = item % NS * VD, hk = h / p.G;
         const int32_t chunks = (sg.tokens + kChunk - 1) / kChunk;
         auto load_k = [&](int32_t c) {
-            if (issuer || c >= chunks) return;
+            if (warp >= T / 32 || c >= chunks) return;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
             load_rows<D / 8, T>(base + (c & 1) * S::KB, p.k + (t0 * H_kv + hk) * D, static_cast<int64_t>(H_kv) * D,
                                 sg.tokens - c * kChunk, tid);
         };
         auto load_v = [&](int32_t c) {
-            if (issuer || c >= chunks) return;
+            if (warp >= T / 32 || c >= chunks) return;
             const int64_t t0 = sg.token + static_cast<int64_t>(c) * kChunk;
             load_rows<VD / 8, T>(base + S::AT_V + c % 3 * S::VB, p.v + (t0 * H_kv + hk) * D + dv0,
                                  static_cast<int64_t>(H_kv) * D, sg.tokens - c * kChunk, tid);
@@ -603,23 +604,24 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
         load_k(0);
         load_v(1);
         cp_async_commit();
-        if (!issuer)
+        if (warp < T / 32)
             for (int32_t c = warp; c < chunks; c += T / 32) {
                 const float2 g = chunk_decays(p, sg, h, c, lane);
                 const Sum t = warp_total(in_log2(g.x) + in_log2(g.y));
                 if (lane == 0) totals[c] = t;
             }
-        // the issuing warp works out the factors, a chunk ahead of the terms and two chunks
-        // behind the loads of the decays
+        // factors are worked out a chunk ahead of the terms, from decays loaded a chunk before;
+        // that takes as long as the terms and the fold together, so this warp meets the others
+        // once a chunk only
         float2 g = make_float2(0.f, 0.f);
         __syncthreads();
-        if (issuer) {
+        if (decays) {
             factors(0, chunk_decays(p, sg, h, 0, lane));
             g = chunk_decays(p, sg, h, 1, lane);
         }
         const int64_t state_at = static_cast<int64_t>(FINAL ? __ldg(p.where + sg.req) : sg.slot + 1) * p.H + h;
         float* const dst = (FINAL ? p.state_out : p.slots) + state_at * D * D + dv0;
-        if (FINAL && !issuer) {  // the state before the request, decayed to its end
+        if (FINAL && warp < T / 32) {  // the state before the request, decayed to its end
             Sum t = {0.f, 0.f};
             for (int32_t x = lane; x < chunks; x += 32) t = t + totals[x];
             const float a = exp2f(warp_total(t).h);
@@ -643,12 +645,15 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
             bad = __syncthreads_or(bad);  // v and the factors of chunk c are there
             if (bad) break;
             const uint32_t terms = S::AT_W + (c & 1) * 3 * S::VB;
-            if (!issuer) {
-                decayed_terms<VD, S::VB, 3, T>(smem + S::AT_V + c % 3 * S::VB, smem + terms, fac + (c & 1) * kChunk, tid);
-            } else if (c + 1 < chunks) {
-                factors(c + 1, g);
-                g = chunk_decays(p, sg, h, c + 2, lane);
+            if (decays) {
+                if (c + 1 < chunks) {
+                    factors(c + 1, g);
+                    g = chunk_decays(p, sg, h, c + 2, lane);
+                }
+                continue;
             }
+            if (!issuer)
+                decayed_terms<VD, S::VB, 3, T>(smem + S::AT_V + c % 3 * S::VB, smem + terms, fac + (c & 1) * kChunk, tid);
             cp_async_wait<0>();  // k of chunk c
             fence_proxy_async_smem();
             if (c > 0) {  // the chunk before: done with its k and terms
@@ -656,7 +661,7 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
                 fold(!FINAL && c == 1, nullptr);
             }
             tmem_fence_before();
-            __syncthreads();
+            asm volatile("bar.sync 1, %0;" ::"n"(T + 32) : "memory");
             tmem_fence_after();
             if (issuer) {
                 issue_update<D, 3>(tm, base + terms, base + (c & 1) * S::KB, false);
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kAddThreads + 32, 1) retention_add(const RetPa
             load_v(c + 2);
             cp_async_commit();
         }
-        if (!bad) wait();
+        if (!bad && !decays) wait();
         bad = __syncthreads_or(bad);
         if (bad) break;
         fold(!FINAL && chunks == 1, dst);
@@ -1088,7 +1093,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
     cfg.numAttrs = 1;
     if (cut) {
         cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(kAddThreads + 32);
+        cfg.blockDim = dim3(kAddThreads + 64);
         cfg.dynamicSmemBytes = RetAddShape<D>::SMEM;
         e = cudaLaunchKernelEx(&cfg, retention_add<D, false>, p);
         if (e != cudaSuccess) return e;
@@ -1109,7 +1114,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // requests without slots: their states may lie in the place of those that the outputs
     // start from, so they are written last
-    cfg.blockDim = dim3(kAddThreads + 32);
+    cfg.blockDim = dim3(kAddThreads + 64);
     cfg.dynamicSmemBytes = RetAddShape<D>::SMEM;
     return cudaLaunchKernelEx(&cfg, retention_add<D, true>, p);
 }
