@@ -693,11 +693,13 @@ __global__ void __launch_bounds__(kAddThreads + 64, 1) retention_add(const RetPa
 
 // Outputs, chunk by chunk. Three groups of warps meet three times a chunk:
 //   8 state warps   scale the state and copy it to bf16, then (those whose lanes hold
-//                   tokens) decay P, the others copy the next chunk's k and work out
-//                   factors
+//                   tokens) decay P, the others copy the next chunk's k
 //   8 value warps   work out the terms of v, then copy the next chunk's q and v and write
 //                   the outputs of the chunk before
 //   1 issuing warp  P | O1 and the state's update | O2
+//   1 warp          the next chunk's factors; it meets the others once a chunk (in a loading
+//                   warp they were the longest of its third: 184 us against 181 for 16 sequences
+//                   with 4 prompts, 24000 tokens)
 // so that copies, arithmetic, stores and products of one and the next chunk overlap.
 template <int D>
 struct RetOutShape : RetDims<D> {
@@ -716,7 +718,7 @@ struct RetOutShape : RetDims<D> {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetParams p) {
+__global__ void __launch_bounds__(kOutThreads + 64, 1) retention_out(const RetParams p) {
     using S = RetOutShape<D>;
     constexpr int NS = S::NS, VD = S::VD, F = S::FACTORS * kChunk;
     constexpr int CW = D / 2 < 32 ? D / 2 : 32;  // columns of a step through a state warp's half
@@ -730,7 +732,8 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
     float* const fac = reinterpret_cast<float*>(smem + S::AT_F);
     float2* const whole = reinterpret_cast<float2*>(fac + 4 * F);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool of_state = warp < 8, issuer = warp == 16;
+    const bool of_state = warp < 8, of_value = warp >= 8 && warp < 16, issuer = warp == 16;
+    const bool decays = warp == 17;
     const bool loader = of_state && (warp & 2);   // state warps without tokens: 2, 3, 6, 7
     const int half = (warp >> 2) & 1;             // which half of the columns this warp takes
     const int row = (warp & 3) * 32 + lane;       // its lane of tensor memory
@@ -756,6 +759,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
         if (!bad && !mbar_wait_bounded(bar, ph, kRetWaitNs)) bad = true;
         ph ^= 1;
     };
+    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOutThreads + 32) : "memory"); };
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
 
@@ -779,7 +783,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
             }
             cp_async_commit();
         };
-        const bool copies = loader || (!of_state && !issuer);
+        const bool copies = loader || of_value;
         auto factors = [&](int32_t c, float2 g) {  // from the chunk's decays: one warp
             Sum l0, l1;
             running_sums(g, lane, l0, l1);
@@ -800,9 +804,11 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
         };
         __syncthreads();  // the previous item is done with shared and tensor memory
         if (copies) load(0);
-        if (warp == 8) factors(0, chunk_decays(p, sg, h, 0, lane));
-        if (warp == 9 && chunks > 1) factors(1, chunk_decays(p, sg, h, 1, lane));
-        float2 g = make_float2(0.f, 0.f);  // warps 2 and 3: decays of the next even and odd chunk
+        float2 g = make_float2(0.f, 0.f);  // decays of the chunk after next
+        if (decays) {
+            factors(0, chunk_decays(p, sg, h, 0, lane));
+            g = chunk_decays(p, sg, h, 1, lane);
+        }
         if (of_state) {  // the state before the segment
             const float* src = nullptr;
             const int32_t q = __ldg(p.qsl + sg.req + 1) - __ldg(p.qsl + sg.req);
@@ -870,10 +876,17 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
             }
             if (of_state && pending) wait(&bar_s, ph_s);  // the state before this chunk is complete
             pending = update;
-            if (!of_state && !issuer && c > 0) take_outputs(c - 1);
+            if (of_value && c > 0) take_outputs(c - 1);
             tmem_fence_before();
             bad = __syncthreads_or(bad);  // (1) chunk c, its factors and its place are there
             if (bad) break;
+            if (decays) {  // meets the others here alone
+                if (update) {
+                    factors(c + 1, g);
+                    g = chunk_decays(p, sg, h, c + 2, lane);
+                }
+                continue;
+            }
             tmem_fence_after();
             if (issuer) {  // P = q k^T (128 rows: the upper 64 are not looked at)
 #pragma unroll
@@ -906,7 +919,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
                 fence_proxy_async_smem();
             }
             tmem_fence_before();
-            __syncthreads();  // (2) the state's copy and the terms are complete
+            meet();  // (2) the state's copy and the terms are complete
             tmem_fence_after();
             if (issuer) {  // O1^T = S^T q^T, and the state after the chunk
 #pragma unroll
@@ -918,16 +931,11 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
                     issue_update<D, 2>(tm + S::TS, base + S::AT_W, sk, true);
                     tmem_commit(&bar_s);
                 }
-            } else if (!of_state) {
+            } else if (of_value) {
                 if (c + 1 < chunks) load(c + 1);
                 if (c > 0) write_outputs(c - 1);
             } else if (loader) {
                 if (c + 1 < chunks) load(c + 1);  // its stage: the products of chunk c - 1 are done
-                if (warp < 4) {  // factors of two chunks every other one, from decays loaded the time before
-                    const int32_t x = c + (c & 1 ? 1 : 2) + (warp & 1);
-                    if (!(c & 1)) g = chunk_decays(p, sg, h, x, lane);
-                    else if (x < chunks) factors(x, g);
-                }
             } else {  // weights of token `row` for 32 tokens
                 wait(&bar_p, ph_p);
                 tmem_fence_after();
@@ -972,7 +980,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
                 fence_proxy_async_smem();
             }
             tmem_fence_before();
-            __syncthreads();  // (3) P is in shared memory, its columns are free
+            meet();  // (3) P is in shared memory, its columns are free
             tmem_fence_after();
             if (issuer) {  // O2^T = v^T P^T
 #pragma unroll
@@ -984,7 +992,7 @@ __global__ void __launch_bounds__(kOutThreads + 32, 1) retention_out(const RetPa
             }
         }
         if (!bad) {
-            if (!of_state && !issuer) {
+            if (of_value) {
                 take_outputs(chunks - 1);
                 write_outputs(chunks - 1);
             }
@@ -1108,7 +1116,7 @@ cudaError_t launch_retention(const RetParams& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kOutThreads + 32);
+    cfg.blockDim = dim3(kOutThreads + 64);
     cfg.dynamicSmemBytes = RetOutShape<D>::SMEM;
     e = cudaLaunchKernelEx(&cfg, retention_out<D>, p);
     if (e != cudaSuccess) return e;
