@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kAddThreads + 64, 1) retention_add(const RetPa
     auto wait = [&]() {
         if (!bad && !mbar_wait_bounded(&bar, ph, kRetWaitNs)) bad = true;
         ph ^= 1;
+        __syncwarp();  // the lanes have polled each for itself
         tmem_fence_after();
     };
     // A thread's columns of its lane: a half of D, CW at a time. Products in columns 0.., the
@@ -661,7 +662,8 @@ __global__ void __launch_bounds__(kAddThreads + 64, 1) retention_add(const RetPa
                 fold(!FINAL && c == 1, nullptr);
             }
             tmem_fence_before();
-            asm volatile("bar.sync 1, %0;" ::"n"(T + 32) : "memory");
+            __syncwarp();
+            asm volatile("bar.sync 1, %0;" ::"n"(T + 32) : "memory");  // all but the factors' warp
             tmem_fence_after();
             if (issuer) {
                 issue_update<D, 3>(tm, base + terms, base + (c & 1) * S::KB, false);
@@ -758,8 +760,12 @@ __global__ void __launch_bounds__(kOutThreads + 64, 1) retention_out(const RetPa
     auto wait = [&](uint64_t* bar, uint32_t& ph) {
         if (!bad && !mbar_wait_bounded(bar, ph, kRetWaitNs)) bad = true;
         ph ^= 1;
+        __syncwarp();  // the lanes have polled each for itself
     };
-    auto meet = [] { asm volatile("bar.sync 1, %0;" ::"n"(kOutThreads + 32) : "memory"); };
+    auto meet = [] {  // all but the factors' warp
+        __syncwarp();
+        asm volatile("bar.sync 1, %0;" ::"n"(kOutThreads + 32) : "memory");
+    };
     const int32_t H_kv = p.H / p.G;
     const int32_t items = *p.num_segs * p.H * NS;
 
