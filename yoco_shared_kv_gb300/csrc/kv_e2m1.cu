@@ -15,7 +15,11 @@
 // per token strides over the token's rows of all kv heads, 8 elements (16
 // bytes of bf16) a lane, so that 4 lanes hold a block and its largest
 // magnitude takes two shuffles. K and V go together, two vectors of each in
-// flight a lane.
+// flight a lane. Replayed from a graph, 23900 tokens of 2 kv heads of 256
+// (new rows 49 MB, codes and scales 13 MB): append 14.1 us, 4.4 TB/s, gather
+// 8.8 us, 7.0 TB/s with the pages in L2 (cold they take 17 and 12.5); issue
+// slots are 46% and 44% taken there, DRAM 36% and 14%, so append sits between
+// the two. 64 tokens: 2.5 and 2.1 us, the launch.
 #include "common.cuh"
 
 namespace yoco {
