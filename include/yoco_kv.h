@@ -483,9 +483,10 @@ yoco_status_t yoco_cross_attn_paged_e2m1(const void* q, const void* k_cache, con
  * and its state are left as they were. head_dim 64, 128 or 256. The state and
  * every sum are fp32; outputs of prompts round the weights of a chunk and the
  * state's copy that multiplies q to bf16; the state after the step takes the
- * decayed values in 24 bits. Prompts are worked out in chunks of 64 tokens from
- * their first: a value that is not finite can reach the outputs of its whole
- * chunk, the earlier tokens' too. Results do not depend on timing.
+ * decayed values in 24 bits. Inputs of a token
+ * that are not finite never reach the outputs of earlier tokens; the state that
+ * follows them in a prompt, and outputs that read it, may be NaN where the sums
+ * would be infinite. Results do not depend on timing.
  */
 yoco_status_t yoco_retention(const void* q, const void* k, const void* v, const float* log_decay,
                              int32_t decay_per_token, const float* state, float* state_out,

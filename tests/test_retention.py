@@ -134,6 +134,55 @@ def test_resets_between_tokens():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 2), (256, 1)])
+@pytest.mark.parametrize("at", [0, 1, 37, 64 + 63, 299, 1400])
+def test_values_that_are_not_finite_stay_with_later_tokens(D, G, at):
+    """Token `at` of a prompt has infinities and NaN in v, in one key or in one decay: no other
+    request and no earlier token sees it."""
+    lens = [70, 1500, 1, 130]
+    c = Case(D + at, lens, 2, G, D, before=[0, 3, 5, 0])
+    token = int(c.qsl[1]) + at
+    plain, plain_state = c.run()
+    x = [np.abs(y.float().numpy()) for y in (c.q, c.k, c.v)]
+    mag, _ = ref64.retention(*x, c.decay.numpy(), np.nan_to_num(np.abs(c.state.numpy())), c.where, c.qsl, c.seq, c.scale)
+    end, mine = int(c.qsl[2]), int(c.where[1])
+    others = [int(w) for r, w in enumerate(c.where) if r != 1]
+    for what in ("v", "k", "decay"):
+        x = getattr(c, what)
+        kept = x.clone()
+        if what == "v":
+            x[token, 0, 3], x[token, 0, D - 1] = float("nan"), -float("inf")
+        elif what == "k":
+            x[token, 0, 5] = float("nan")
+        else:
+            x[token, 0] = float("nan")
+        out, after = c.run()
+        setattr(c, what, kept)
+        assert torch.equal(out[:c.qsl[1]], plain[:c.qsl[1]]) and torch.equal(out[end:], plain[end:])
+        assert torch.equal(after[others], plain_state[others])
+        # Tokens before: the same sums. Beside a decay that is not a number a chunk's weights are worked out
+        # another way: each side rounds a weight or an element of the state's copy by 2^-8, its factor by 2^-20
+        # more, and the result by 2^-8.
+        a, b = out[c.qsl[1]:token].float(), plain[c.qsl[1]:token].float()
+        if what != "decay":
+            assert torch.equal(a, b)
+        else:
+            tol = 2 * (2.0 ** -8 + 2.0 ** -16) * mag[c.qsl[1]:token] + 2.0 ** -8 * (a.abs() + b.abs()).double().numpy()
+            assert ((a - b).abs().numpy() <= tol).all()
+        heads = slice(0, G if what != "decay" else 1)  # that read it
+        bad, bad_state = out[token:end, heads], after[mine, heads]
+        if what == "v":
+            assert not torch.isfinite(bad[..., [3, D - 1]]).any() and not torch.isfinite(bad_state[..., [3, D - 1]]).any()
+            rest = [d for d in range(D) if d not in (3, D - 1)]
+            assert torch.equal(bad[..., rest], plain[token:end, heads][..., rest])
+            assert torch.equal(bad_state[..., rest], plain_state[mine, heads][..., rest])
+        else:
+            assert torch.isnan(bad).all()
+            assert torch.isnan(bad_state[:, 5] if what == "k" else bad_state).all()
+        assert torch.equal(out[token:end, heads.stop:], plain[token:end, heads.stop:])
+
+
+@pytest.mark.gpu
 def test_a_prompt_equals_its_tokens():
     """Chunks, two calls, and single tokens walk the same recurrence (each checked against 64 bits)."""
     from yoco_shared_kv_gb300 import _native as N

@@ -27,8 +27,8 @@
 // Measured, replayed from a graph. Single tokens of 64 requests, 8 heads of
 // 256: 43.9 us, 6.1 TB/s on the states' 269 MB (90% of what a copy reaches);
 // of 5, 8 heads of 128: 3.2 us, the launch. 16 single tokens and 4 prompts of
-// 1024..4096, 8 heads of 256: 182 us, where the bytes take 36 and the products
-// 11; one prompt of 16384, 8 heads of 128: 84 us (12 and 5). Of the prompts'
+// 1024..4096, 8 heads of 256: 186 us, where the bytes take 36 and the products
+// 11; one prompt of 16384, 8 heads of 128: 83 us (12 and 5). Of the prompts'
 // time the outputs take half, the segments' states a third, the scan a tenth,
 // the plan 4%. A walk without segments reads every token once and needs no
 // scan, but has 64 CTAs for the first and 8 for the second: at the time of a
@@ -473,6 +473,34 @@ __device__ __forceinline__ void decayed_terms(const uint8_t* v, uint8_t* terms, 
     }
 }
 
+// A value that is not finite makes its dim's products with the weights NaN for all of a chunk's
+// tokens, the earlier ones (weight 0) too. Rare: a warp whose lanes (value dim dv each) meet NaN
+// (`again`) puts sum_(j <= t) P[t][j] v[j][dv] in their place, 32 tokens from t0 on at `at`. A call
+// of its own, so that it takes no registers from the loop.
+__device__ __noinline__ void sum_again(uint32_t at, bool again, const uint8_t* weights, const uint8_t* v, int t0,
+                                       int dv) {
+#pragma unroll 1
+    for (int b = 0; b < 32; b += 16) {
+        uint32_t x[16];
+        tmem_ld(at + b, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (!again) continue;
+            const int t = t0 + b + i;
+            float a = 0.f;
+#pragma unroll 1
+            for (int j = 0; j <= t; ++j)
+                a = fmaf(__bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(weights + block_at(t, j >> 3) + (j & 7) * 2)),
+                         __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + block_at(j, dv >> 3) + (dv & 7) * 2)), a);
+            x[i] = __float_as_uint(a);
+        }
+        __syncwarp();
+        tmem_st(at + b, x);
+        tmem_st_wait();
+    }
+}
+
 // S^T (+)= (decayed v)^T k in TERMS bf16 terms, the smallest first: the tensor cores cut each
 // sum to the accumulator's 24 bits (towards zero), which costs nothing while it is small. The
 // issuing warp.
@@ -494,16 +522,18 @@ __device__ __forceinline__ float2 chunk_decays(const RetParams& p, const RetSeg&
     return make_float2(2 * lane < left ? decay_of(p, t0 + 2 * lane, h) : 0.f,
                        2 * lane + 1 < left ? decay_of(p, t0 + 2 * lane + 1, h) : 0.f);
 }
-// Running sums over the chunk, up to and with tokens 2l and 2l + 1.
+// Running sums over the chunk, up to and with tokens 2l and 2l + 1. (No sum takes a later token's
+// decay in and out again: one that is not a number stays with the tokens from its own on.)
 __device__ __forceinline__ void running_sums(float2 g, int lane, Sum& l0, Sum& l1) {
-    const Sum g1 = in_log2(g.y);
-    l1 = in_log2(g.x) + g1;
+    const Sum g0 = in_log2(g.x);
+    l1 = g0 + in_log2(g.y);
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const Sum x = shfl_up(l1, off);
         if (lane >= off) l1 = l1 + x;
     }
-    l0 = l1 + Sum{-g1.h, -g1.l};
+    const Sum before = shfl_up(l1, 1);
+    l0 = lane > 0 ? g0 + before : g0;
 }
 
 // States. Without FINAL, what each segment adds, from zero, into its slot; with FINAL, the
@@ -867,6 +897,16 @@ __global__ void __launch_bounds__(kOutThreads + 64, 1) retention_out(const RetPa
                 tmem_ld(tm + lanes + S::TO1 + half * HT + b * 16, o1);
                 tmem_ld(tm + lanes + S::TO2 + half * HT + b * 16, o2);
                 tmem_ld_wait();
+                if (b == 0) {
+                    const bool again = row < VD && isnan(__uint_as_float(o2[0]));
+                    if (__any_sync(0xffffffffu, again)) {
+                        sum_again(tm + lanes + S::TO2 + half * HT, again, smem + S::AT_P,
+                                  smem + (c & 1) * S::STAGE + 2 * S::KB, half * HT, row);
+                        tmem_ld(tm + lanes + S::TO1 + half * HT, o1);
+                        tmem_ld(tm + lanes + S::TO2 + half * HT, o2);
+                        tmem_ld_wait();
+                    }
+                }
 #pragma unroll
                 for (int t = 0; t < 16; t += 2) {
                     const float2 e = *reinterpret_cast<const float2*>(et + b * 16 + t);
